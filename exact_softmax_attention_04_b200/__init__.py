@@ -31,7 +31,10 @@ EXPORTS = ("attn_fwd", "attn_fwd_gqa", "attn_fwd_host", "attn_host_staging_relea
            "attn_sync_status", "attn_strerror", "attn_attended_pairs", "attn_fwd_host_noalloc",
            "attn_bwd", "attn_bwd_gqa", "attn_bwd_workspace_bytes", "attn_decode",
            "attn_decode_workspace_bytes", "attn_decode_multi", "attn_decode_multi_workspace_bytes",
-           "attn_fwd_blocklocal", "attn_bwd_blocklocal", "attn_fwd_schedule", "attn_fwd_schedule_for")
+           "attn_fwd_blocklocal", "attn_bwd_blocklocal", "attn_fwd_schedule", "attn_fwd_schedule_for",
+           "attn_decode_paged", "attn_decode_paged_workspace_bytes", "attn_decode_latent",
+           "attn_decode_latent_workspace_bytes", "attn_pages_append", "attn_pages_workspace_bytes",
+           "attn_pages_reserve", "attn_pages_fork", "attn_pages_free", "attn_pages_compact")
 
 
 class AttnError(RuntimeError):
@@ -94,6 +97,27 @@ def load_library(path: str) -> ctypes.CDLL:
     lib.attn_decode_multi.restype = i
     lib.attn_decode_multi_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
     lib.attn_decode_multi_workspace_bytes.restype = i64
+    size = ctypes.c_size_t
+    lib.attn_decode_paged.argtypes = [vp] * 9 + [size] + [i] * 9 + [f, vp]
+    lib.attn_decode_paged.restype = i
+    lib.attn_decode_paged_workspace_bytes.argtypes = [i] * 7
+    lib.attn_decode_paged_workspace_bytes.restype = i64
+    lib.attn_decode_latent.argtypes = [vp] * 8 + [size] + [i] * 7 + [f, vp]
+    lib.attn_decode_latent.restype = i
+    lib.attn_decode_latent_workspace_bytes.argtypes = [i] * 6
+    lib.attn_decode_latent_workspace_bytes.restype = i64
+    lib.attn_pages_append.argtypes = [vp] * 10 + [i] * 7 + [vp]
+    lib.attn_pages_append.restype = i
+    lib.attn_pages_workspace_bytes.argtypes = [i] * 3
+    lib.attn_pages_workspace_bytes.restype = i64
+    lib.attn_pages_reserve.argtypes = [vp] * 6 + [size] + [i] * 5 + [vp]
+    lib.attn_pages_reserve.restype = i
+    lib.attn_pages_fork.argtypes = [vp] * 11 + [size] + [i] * 7 + [vp]
+    lib.attn_pages_fork.restype = i
+    lib.attn_pages_free.argtypes = [vp] * 4 + [i] * 4 + [vp]
+    lib.attn_pages_free.restype = i
+    lib.attn_pages_compact.argtypes = [vp] * 9 + [size] + [i] * 6 + [vp]
+    lib.attn_pages_compact.restype = i
     return lib
 
 
@@ -358,6 +382,329 @@ def attn_decode_multi(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode_multi")
     return out, lse
+
+
+# ---------------------------------------------------------------------------
+# Paged caches (see "Paged caches" in include/attn.h)
+
+def _check_ints(device: torch.device, **tensors) -> None:
+    """Each of ``tensors`` (name=(tensor, shape)) an int32 tensor on ``device``."""
+    for name, (t, shape) in tensors.items():
+        if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or t.shape != shape:
+            raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on the pages' device")
+
+
+def _check_pool(name: str, pool: torch.Tensor) -> None:
+    if pool.dtype != torch.bfloat16 or not pool.is_cuda:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor")
+    if pool.stride(-1) != 1 and pool.shape[-1] != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+
+
+def _strides(t: torch.Tensor, at_least: int):
+    """The strides of all dimensions but the last as a C array, None if t is
+    contiguous. A dimension of one element is never stepped along: its stride
+    is given as ``at_least``."""
+    if t.is_contiguous():
+        return None
+    n = t.dim() - 1
+    return (ctypes.c_int64 * n)(*(t.stride(j) if t.shape[j] > 1 else at_least for j in range(n)))
+
+
+def _pools(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor]):
+    """(Hkv, num_pages, page_size, d, strides) of one or two pools."""
+    _check_pool("k_pages", k_pages)
+    if v_pages is None:
+        if k_pages.dim() != 3:
+            raise ValueError("a pool of latent rows must be [num_pages, page_size, d]")
+        k_pages = k_pages.unsqueeze(1)
+    else:
+        _check_pool("v_pages", v_pages)
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.device != v_pages.device:
+            raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, d], alike and on one device")
+    P, Hkv, page, d = k_pages.shape
+    strides = _strides(k_pages, d)
+    if v_pages is not None:
+        other = _strides(v_pages, d)
+        if (strides is None) != (other is None) or (strides is not None and list(strides) != list(other)):
+            raise ValueError("k_pages and v_pages must have the same strides")
+    return Hkv, P, page, d, strides
+
+
+def _outputs(q: torch.Tensor, width: int, out: Optional[torch.Tensor], lse: Optional[torch.Tensor]):
+    shape, rows = q.shape[:-1] + (width,), q.shape[:-1]
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    elif out.shape != shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != q.device:
+        raise ValueError(f"out must be a contiguous bf16 tensor {list(shape)} on q's device")
+    if lse is None:
+        lse = torch.empty(rows, dtype=torch.float32, device=q.device)
+    elif lse.shape != rows or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != q.device:
+        raise ValueError(f"lse must be a contiguous fp32 tensor {list(rows)} on q's device")
+    return out, lse
+
+
+def _scratch(workspace: Optional[torch.Tensor], need: int, device: torch.device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the pages' device")
+    return workspace
+
+
+def decode_paged_workspace_bytes(B: int, H: int, Hkv: int, T: int, max_pages: int, page_size: int, d: int) -> int:
+    r = int(lib().attn_decode_paged_workspace_bytes(int(B), int(H), int(Hkv), int(T), int(max_pages),
+                                                    int(page_size), int(d)))
+    if r < 0:
+        raise ValueError("unsupported or invalid shape for attn_decode_paged")
+    return r
+
+
+def attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                      lens: torch.Tensor, window: int = -1, scale: Optional[float] = None,
+                      out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of each sequence's T newest tokens over its paged cache.
+
+    q: bf16 CUDA tensor [B, H, T, d], or [B, H, d] for one token; k_pages,
+    v_pages: bf16 [num_pages, Hkv, page_size, d] of any strides whose last is
+    1 (a token-major pool is passed transposed); page_table int32
+    [B, max_pages]; lens int32 [B], the tokens each sequence holds, the new
+    ones included. window < 0: every earlier position. Returns (o shaped like
+    q, lse fp32 without the last dimension); a token that sees no position
+    gets 0 and -inf. See include/attn.h."""
+    Hkv, P, page, d, strides = _pools(k_pages, v_pages)
+    if q.dtype != torch.bfloat16 or q.device != k_pages.device or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 tensor on the pages' device")
+    if q.dim() not in (3, 4) or q.shape[-1] != d:
+        raise ValueError("q must be [B, H, T, d] or [B, H, d] with the pages' d")
+    B, H, T = q.shape[0], q.shape[1], q.shape[2] if q.dim() == 4 else 1
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    width = page_table.shape[1]
+    _check_ints(q.device, page_table=(page_table, (B, width)), lens=(lens, (B,)))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if workspace is None:
+        workspace = _scratch(None, decode_paged_workspace_bytes(B, H, Hkv, T, width, page, d), q.device)
+    else:
+        _scratch(workspace, 0, q.device)
+    out, lse = _outputs(q, d, out, lse)
+    with torch.cuda.device(q.device):
+        rc = lib().attn_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), strides,
+                                     page_table.data_ptr(), lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(), B, H, Hkv,
+                                     T, P, page, width, int(window), d, float(scale), _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_decode_paged")
+    return out, lse
+
+
+def decode_latent_workspace_bytes(B: int, H: int, T: int, max_pages: int, page_size: int, rank: int) -> int:
+    r = int(lib().attn_decode_latent_workspace_bytes(int(B), int(H), int(T), int(max_pages), int(page_size),
+                                                     int(rank)))
+    if r < 0:
+        raise ValueError("unsupported or invalid shape for attn_decode_latent")
+    return r
+
+
+def attn_decode_latent(q: torch.Tensor, pages: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                       scale: float, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of each sequence's T newest tokens over a paged cache of one
+    latent vector a token (latent attention, absorbed form).
+
+    q: bf16 CUDA tensor [B, H, T, rank + 64], or [B, H, rank + 64] for one
+    token; pages: bf16 [num_pages, page_size, rank + 64], last stride 1;
+    page_table int32 [B, max_pages]; lens int32 [B]. The first `rank` elements
+    of a row are the values of every head. ``scale`` is the expanded heads' own
+    (rank does not tell it). Returns (o [B, H, T, rank] or [B, H, rank], lse
+    fp32). See include/attn.h."""
+    _, P, page, D, strides = _pools(pages, None)
+    if q.dtype != torch.bfloat16 or q.device != pages.device or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 tensor on the pages' device")
+    if q.dim() not in (3, 4) or q.shape[-1] != D or D <= 64:
+        raise ValueError("q must be [B, H, T, rank + 64] or [B, H, rank + 64] with the pages' row length")
+    B, H, T = q.shape[0], q.shape[1], q.shape[2] if q.dim() == 4 else 1
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    width, rank = page_table.shape[1], D - 64
+    _check_ints(q.device, page_table=(page_table, (B, width)), lens=(lens, (B,)))
+    if workspace is None:
+        workspace = _scratch(None, decode_latent_workspace_bytes(B, H, T, width, page, rank), q.device)
+    else:
+        _scratch(workspace, 0, q.device)
+    out, lse = _outputs(q, rank, out, lse)
+    if strides is not None:
+        strides = (ctypes.c_int64 * 2)(strides[0], strides[2])
+    with torch.cuda.device(q.device):
+        rc = lib().attn_decode_latent(q.data_ptr(), pages.data_ptr(), strides, page_table.data_ptr(),
+                                      lens.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(), B, H, T, P, page, width, rank,
+                                      float(scale), _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_decode_latent")
+    return out, lse
+
+
+def pages_append(k: torch.Tensor, v: Optional[torch.Tensor], k_pages: torch.Tensor,
+                 v_pages: Optional[torch.Tensor], page_table: torch.Tensor, pos: torch.Tensor,
+                 count: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Write new tokens' rows to their pages, in place.
+
+    k, v: bf16 [B, Hkv, T, d] of any strides whose last is 1; token u < count[b]
+    (default T) goes to position pos[b] + u. A pool of latent rows
+    [num_pages, page_size, d] takes k [B, 1, T, d] and v = v_pages = None.
+    page_table int32 [B, max_pages], pos and count int32 [B]."""
+    if (v is None) != (v_pages is None):
+        raise ValueError("v and v_pages go together")
+    Hkv, P, page, d, strides = _pools(k_pages, v_pages)
+    news = [(k, "k")] + ([(v, "v")] if v is not None else [])
+    for t, name in news:
+        if t.dtype != torch.bfloat16 or t.device != k_pages.device or t.dim() != 4 or t.shape != k.shape or \
+                t.shape[1] != Hkv or t.shape[3] != d or t.stride(3) != 1:
+            raise ValueError(f"{name} must be a bf16 tensor [B, Hkv, T, d] on the pages' device, last stride 1")
+    B, _, T, _ = k.shape
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    width = page_table.shape[1]
+    _check_ints(k.device, page_table=(page_table, (B, width)), pos=(pos, (B,)))
+    if count is not None:
+        _check_ints(k.device, count=(count, (B,)))
+    with torch.cuda.device(k.device):
+        rc = lib().attn_pages_append(k.data_ptr(), None if v is None else v.data_ptr(), _strides(k, 0),
+                                     None if v is None else _strides(v, 0), k_pages.data_ptr(),
+                                     None if v is None else v_pages.data_ptr(), strides, page_table.data_ptr(),
+                                     pos.data_ptr(), None if count is None else count.data_ptr(), B, Hkv, T, P,
+                                     page, width, d, _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_pages_append")
+
+
+def pages_workspace_bytes(n: int, num_rows: int, num_pages: int) -> int:
+    r = int(lib().attn_pages_workspace_bytes(int(n), int(num_rows), int(num_pages)))
+    if r < 0:
+        raise ValueError("unsupported or invalid shape for the page operations")
+    return r
+
+
+def _check_state(device: torch.device, page_table: torch.Tensor, refs: torch.Tensor,
+                 lens: Optional[torch.Tensor] = None, **lists) -> None:
+    if page_table.dim() != 2 or refs.dim() != 1 or not refs.is_cuda:
+        raise ValueError("page_table must be [num_rows, max_pages] and refs a CUDA tensor [num_pages]")
+    _check_ints(device, page_table=(page_table, page_table.shape), refs=(refs, refs.shape))
+    if lens is not None:
+        _check_ints(device, lens=(lens, page_table.shape[:1]))
+    for name, t in lists.items():
+        if t.dim() != 1:
+            raise ValueError(f"{name} must have one dimension")
+        _check_ints(device, **{name: (t, t.shape)})
+
+
+def pages_reserve(page_table: torch.Tensor, refs: torch.Tensor, rows: torch.Tensor, want: torch.Tensor,
+                  page_size: int, workspace: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Give rows[i] (int32 [n]) pages for want[i] tokens in all, in place: its
+    entries below ceil(want / page_size) without a page get the lowest free
+    ones (refs 0), whose counts become 1. Returns granted int32 [n]: 1, or 0
+    where the free pages did not suffice or the request was not valid."""
+    _check_state(refs.device, page_table, refs, rows=rows, want=want)
+    if rows.shape != want.shape:
+        raise ValueError("rows and want must be alike")
+    n, (R, width), P = rows.shape[0], page_table.shape, refs.shape[0]
+    granted = torch.empty_like(rows)
+    if n == 0:
+        return granted
+    if workspace is None:
+        workspace = _scratch(None, pages_workspace_bytes(n, R, P), refs.device)
+    else:
+        _scratch(workspace, 0, refs.device)
+    with torch.cuda.device(refs.device):
+        rc = lib().attn_pages_reserve(page_table.data_ptr(), refs.data_ptr(), rows.data_ptr(), want.data_ptr(),
+                                      granted.data_ptr(), workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(), n, R, P, int(page_size), width,
+                                      _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_pages_reserve")
+    return granted
+
+
+def pages_fork(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], page_table: torch.Tensor,
+               lens: torch.Tensor, refs: torch.Tensor, parents: torch.Tensor, children: torch.Tensor,
+               workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+               ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Make the empty rows children[i] copies of rows parents[i], in place: full
+    pages are shared (refs rise), a partly filled last page is copied to the
+    lowest free page. Returns (fresh, granted), int32 [n]: the page taken or
+    -1, and 1 or 0. See include/attn.h."""
+    Hkv, P, page, d, strides = _pools(k_pages, v_pages)
+    _check_state(k_pages.device, page_table, refs, lens, parents=parents, children=children)
+    if refs.shape[0] != P or parents.shape != children.shape:
+        raise ValueError("refs must have one count a page, and parents and children must be alike")
+    n, (R, width) = parents.shape[0], page_table.shape
+    fresh, granted = torch.empty_like(parents), torch.empty_like(parents)
+    if n == 0:
+        return fresh, granted
+    if workspace is None:
+        workspace = _scratch(None, pages_workspace_bytes(n, R, P), refs.device)
+    else:
+        _scratch(workspace, 0, refs.device)
+    with torch.cuda.device(refs.device):
+        rc = lib().attn_pages_fork(k_pages.data_ptr(), None if v_pages is None else v_pages.data_ptr(), strides,
+                                   page_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), parents.data_ptr(),
+                                   children.data_ptr(), fresh.data_ptr(), granted.data_ptr(), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), n, R, Hkv, P, page, width, d,
+                                   _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_pages_fork")
+    return fresh, granted
+
+
+def pages_free(page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, rows: torch.Tensor,
+               stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Empty rows (int32 [n]) in place: their pages' counts fall, their entries
+    become -1 and their lengths 0."""
+    _check_state(refs.device, page_table, refs, lens, rows=rows)
+    n, (R, width) = rows.shape[0], page_table.shape
+    if n == 0:
+        return
+    with torch.cuda.device(refs.device):
+        rc = lib().attn_pages_free(page_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), rows.data_ptr(), n, R,
+                                   refs.shape[0], width, _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_pages_free")
+
+
+def pages_compact(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], page_table: torch.Tensor,
+                  refs: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                  workspace: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Move the live pages (refs above 0) to the front of the pools, in place,
+    and rename them in the table and the counts: in place, or into ``out``
+    (table, refs). Returns the number of live pages, int32 [1] on the device."""
+    Hkv, P, page, d, strides = _pools(k_pages, v_pages)
+    _check_state(k_pages.device, page_table, refs)
+    if refs.shape[0] != P:
+        raise ValueError("refs must have one count a page")
+    R, width = page_table.shape
+    table_out, refs_out = (page_table, refs) if out is None else out
+    _check_ints(refs.device, table_out=(table_out, page_table.shape), refs_out=(refs_out, refs.shape))
+    live = torch.empty(1, dtype=torch.int32, device=refs.device)
+    if workspace is None:
+        workspace = _scratch(None, pages_workspace_bytes(0, R, P), refs.device)
+    else:
+        _scratch(workspace, 0, refs.device)
+    with torch.cuda.device(refs.device):
+        rc = lib().attn_pages_compact(k_pages.data_ptr(), None if v_pages is None else v_pages.data_ptr(), strides,
+                                      page_table.data_ptr(), refs.data_ptr(), table_out.data_ptr(),
+                                      refs_out.data_ptr(), live.data_ptr(), workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(), R, Hkv, P, page, width, d,
+                                      _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_pages_compact")
+    return live
 
 
 def attn_fwd_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float] = None,

@@ -1,0 +1,199 @@
+// attn_pages_api.cu - host side of the paged cache's upkeep: argument checks,
+// workspace layout, launches. Contracts in include/attn.h.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "attn.h"
+#include "attn_host.h"
+#include "attn_pages_kernel.cuh"
+
+namespace {
+
+using namespace attn_host;
+using namespace attn_sm100;
+
+// The pages' planning kernels sum up to 1024 page counts in 32 bits.
+constexpr int kMaxPages = (1 << 21) - 1;
+
+int check_pools(PagePools *p, const void *k_pages, const void *v_pages, const int64_t *strides, int Hkv,
+                int num_pages, int page_size, int d)
+{
+    if (!k_pages || !aligned(k_pages, 16) || !aligned(v_pages, 16)) return ATTN_ERR_INVALID;
+    if (Hkv <= 0 || num_pages <= 0 || page_size <= 0 || d <= 0) return ATTN_ERR_INVALID;
+    if (d % 8 != 0 || d > 1024 || num_pages > kMaxPages) return ATTN_ERR_UNSUPPORTED;
+    // a page's 16-byte units are counted in 32 bits
+    if (static_cast<int64_t>(2) * Hkv * page_size > INT_MAX / (d / 8)) return ATTN_ERR_UNSUPPORTED;
+    const int64_t packed[3] = {static_cast<int64_t>(Hkv) * page_size * d, static_cast<int64_t>(page_size) * d, d};
+    const int64_t *const s = strides ? strides : packed;
+    for (int i = 0; i < 3; ++i)
+        if (s[i] < d || s[i] % 8 != 0) return ATTN_ERR_INVALID;
+    p->pool[0] = static_cast<uint4 *>(const_cast<void *>(k_pages));
+    p->pool[1] = static_cast<uint4 *>(const_cast<void *>(v_pages));
+    p->npools = v_pages ? 2 : 1;
+    p->page_stride = s[0] / 8;
+    p->head_stride = s[1] / 8;
+    p->token_stride = s[2] / 8;
+    p->heads = Hkv;
+    p->vecs = d / 8;
+    p->num_pages = num_pages;
+    p->page_size = page_size;
+    return ATTN_OK;
+}
+
+int check_ints(std::initializer_list<const void *> ptrs)
+{
+    for (const void *p : ptrs)
+        if (!p || !aligned(p, 4)) return ATTN_ERR_INVALID;
+    return ATTN_OK;
+}
+
+// Workspace in ints: owners by row, two values and a page per request (or per
+// page for reserve and compact), ranks, a few scalars.
+int64_t workspace_ints(int n, int num_rows, int num_pages)
+{
+    return static_cast<int64_t>(num_rows) + 2 * static_cast<int64_t>(n) + 3 * static_cast<int64_t>(num_pages) + 64;
+}
+
+int launched() { return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" int64_t attn_pages_workspace_bytes(int n, int num_rows, int num_pages)
+{
+    if (n < 0 || num_rows <= 0 || num_pages <= 0 || num_pages > kMaxPages) return -1;
+    return 4 * workspace_ints(n, num_rows, num_pages);
+}
+
+extern "C" int attn_pages_append(const void *k, const void *v, const int64_t *k_strides, const int64_t *v_strides,
+                                 void *k_pages, void *v_pages, const int64_t *kv_strides, const int *page_table,
+                                 const int *pos, const int *count, int B, int Hkv, int T, int num_pages,
+                                 int page_size, int max_pages, int d, void *stream)
+{
+    AppendParams a;
+    int rc = check_pools(&a.p, k_pages, v_pages, kv_strides, Hkv, num_pages, page_size, d);
+    if (rc != ATTN_OK) return rc;
+    if (!k || !aligned(k, 16) || !aligned(v, 16) || (v == nullptr) != (v_pages == nullptr)) return ATTN_ERR_INVALID;
+    if (B <= 0 || T <= 0 || max_pages <= 0) return ATTN_ERR_INVALID;
+    rc = check_ints({page_table, pos});
+    if (rc != ATTN_OK || !aligned(count, 4)) return ATTN_ERR_INVALID;
+    if (B > 65535 || static_cast<int64_t>(Hkv) * T > INT_MAX / d) return ATTN_ERR_UNSUPPORTED;
+    const int64_t packed[3] = {static_cast<int64_t>(Hkv) * T * d, static_cast<int64_t>(T) * d, d};
+    for (int i = 0; i < 2; ++i) {
+        const int64_t *s = i == 0 ? k_strides : v_strides;
+        if (!s) s = packed;
+        for (int j = 0; j < 3; ++j)
+            if (s[j] < 0 || s[j] % 8 != 0) return ATTN_ERR_INVALID;
+        a.src[i] = static_cast<const uint4 *>(i == 0 ? k : v);
+        a.sb[i] = s[0] / 8;
+        a.sh[i] = s[1] / 8;
+        a.st[i] = s[2] / 8;
+    }
+    a.table = page_table;
+    a.pos = pos;
+    a.count = count;
+    a.T = T;
+    a.max_pages = max_pages;
+    const int per = std::max(1, 4 * APPEND_THREADS / (a.p.heads * a.p.vecs));
+    const dim3 grid(static_cast<unsigned>((T + per - 1) / per), static_cast<unsigned>(B));
+    pages_append_kernel<<<grid, APPEND_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(a, per);
+    return launched();
+}
+
+extern "C" int attn_pages_reserve(int *page_table, int *refs, const int *rows, const int *want, int *granted,
+                                  void *workspace, size_t workspace_bytes, int n, int num_rows, int num_pages,
+                                  int page_size, int max_pages, void *stream)
+{
+    if (n < 0 || num_rows <= 0 || num_pages <= 0 || page_size <= 0 || max_pages <= 0) return ATTN_ERR_INVALID;
+    if (num_pages > kMaxPages) return ATTN_ERR_UNSUPPORTED;
+    if (n == 0) return ATTN_OK;
+    if (check_ints({page_table, refs, rows, want, granted, workspace}) != ATTN_OK) return ATTN_ERR_INVALID;
+    if (workspace_bytes < static_cast<size_t>(4 * workspace_ints(n, num_rows, num_pages))) return ATTN_ERR_INVALID;
+    ReserveParams a;
+    a.t = {page_table, nullptr, refs, num_rows, max_pages};
+    a.rows = rows;
+    a.want = want;
+    a.granted = granted;
+    a.owner = static_cast<int *>(workspace);
+    a.first = a.owner + num_rows;
+    a.list = a.first + n;
+    a.n = n;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    pages_reserve_kernel<<<1, PLAN_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    return launched();
+}
+
+extern "C" int attn_pages_fork(void *k_pages, void *v_pages, const int64_t *kv_strides, int *page_table, int *lens,
+                               int *refs, const int *parents, const int *children, int *fresh, int *granted,
+                               void *workspace, size_t workspace_bytes, int n, int num_rows, int Hkv, int num_pages,
+                               int page_size, int max_pages, int d, void *stream)
+{
+    ForkParams a;
+    const int rc = check_pools(&a.p, k_pages, v_pages, kv_strides, Hkv, num_pages, page_size, d);
+    if (rc != ATTN_OK) return rc;
+    if (n < 0 || num_rows <= 0 || max_pages <= 0) return ATTN_ERR_INVALID;
+    if (n == 0) return ATTN_OK;
+    if (check_ints({page_table, lens, refs, parents, children, fresh, granted, workspace}) != ATTN_OK)
+        return ATTN_ERR_INVALID;
+    if (workspace_bytes < static_cast<size_t>(4 * workspace_ints(n, num_rows, num_pages))) return ATTN_ERR_INVALID;
+    a.t = {page_table, lens, refs, num_rows, max_pages};
+    a.parents = parents;
+    a.children = children;
+    a.fresh = fresh;
+    a.granted = granted;
+    a.owner = static_cast<int *>(workspace);
+    a.length = a.owner + num_rows;
+    a.list = a.length + n;
+    a.n = n;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    pages_fork_plan_kernel<<<1, PLAN_THREADS, 0, st>>>(a);
+    if (launched() != ATTN_OK) return ATTN_ERR_CUDA;
+    const int64_t units = static_cast<int64_t>(a.p.npools) * Hkv * page_size * a.p.vecs;
+    const unsigned split = static_cast<unsigned>(std::min<int64_t>(64, (units + 1023) / 1024));
+    pages_fork_kernel<<<dim3(static_cast<unsigned>(n), split), FORK_THREADS, 0, st>>>(a);
+    return launched();
+}
+
+extern "C" int attn_pages_free(int *page_table, int *lens, int *refs, const int *rows, int n, int num_rows,
+                               int num_pages, int max_pages, void *stream)
+{
+    if (n < 0 || num_rows <= 0 || num_pages <= 0 || max_pages <= 0) return ATTN_ERR_INVALID;
+    if (n == 0) return ATTN_OK;
+    if (check_ints({page_table, lens, refs, rows}) != ATTN_OK) return ATTN_ERR_INVALID;
+    const PageTables t = {page_table, lens, refs, num_rows, max_pages};
+    pages_free_kernel<<<static_cast<unsigned>(n), FREE_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(t, rows,
+                                                                                                       num_pages);
+    return launched();
+}
+
+extern "C" int attn_pages_compact(void *k_pages, void *v_pages, const int64_t *kv_strides, const int *page_table,
+                                  const int *refs, int *table_out, int *refs_out, int *live, void *workspace,
+                                  size_t workspace_bytes, int num_rows, int Hkv, int num_pages, int page_size,
+                                  int max_pages, int d, void *stream)
+{
+    CompactParams a;
+    const int rc = check_pools(&a.p, k_pages, v_pages, kv_strides, Hkv, num_pages, page_size, d);
+    if (rc != ATTN_OK) return rc;
+    if (num_rows <= 0 || max_pages <= 0) return ATTN_ERR_INVALID;
+    if (check_ints({page_table, refs, table_out, refs_out, live, workspace}) != ATTN_OK) return ATTN_ERR_INVALID;
+    if (workspace_bytes < static_cast<size_t>(4 * workspace_ints(0, num_rows, num_pages))) return ATTN_ERR_INVALID;
+    a.table = page_table;
+    a.refs = refs;
+    a.table_out = table_out;
+    a.refs_out = refs_out;
+    a.live = live;
+    a.holes = static_cast<int *>(workspace);
+    a.movers = a.holes + num_pages;
+    a.rank = a.movers + num_pages;
+    a.moves = a.rank + num_pages;
+    a.cells = static_cast<int64_t>(num_rows) * max_pages;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    pages_compact_plan_kernel<<<1, PLAN_THREADS, 0, st>>>(a);
+    if (launched() != ATTN_OK) return ATTN_ERR_CUDA;
+    pages_compact_kernel<<<148 * 8, COMPACT_THREADS, 0, st>>>(a);
+    return launched();
+}

@@ -1,7 +1,9 @@
 /*
  * attn.h - C ABI of the B200 (sm_100a) exact softmax attention library
  * (libattn_b200.so): forward pass (device or host buffers), grouped-query and
- * block-local forms, backward pass, decode against rolling key/value caches.
+ * block-local forms, backward pass, decode against rolling key/value caches
+ * and against paged ones (keys and values, or one latent vector a token),
+ * and the upkeep of a paged cache.
  *
  * The operation (all entry points that compute):
  *
@@ -403,6 +405,214 @@ ATTN_API int attn_decode_multi(const void *q, const void *k_cache, const void *v
  * invalid or unsupported. */
 ATTN_API int64_t attn_decode_multi_workspace_bytes(int B, int H, int Hkv, int T, int W, int window,
                                                    int d);
+
+/*
+ * Paged caches
+ *
+ * A paged cache keeps the rows of many sequences in one pool of pages, so
+ * that a sequence takes memory as it grows and several can share a prefix:
+ *
+ *   pool        : bf16, num_pages pages of page_size token rows for each of
+ *                 Hkv key/value heads. `kv_strides` (host array, may be NULL)
+ *                 holds the strides in elements between pages, heads and
+ *                 tokens: multiples of 8, at least d. NULL: contiguous
+ *                 [num_pages, Hkv, page_size, d]. Keys and values are two
+ *                 pools of the same strides.
+ *   page_table  : device, int32 [rows, max_pages]: position p of row r lies
+ *                 in page page_table[r, p / page_size], slot p % page_size.
+ *                 An entry outside [0, num_pages) (by custom -1) is no page:
+ *                 nothing is read or written through it.
+ *   lens        : device, int32 [rows]: tokens cached (a negative one counts
+ *                 as 0; the decode entry points read one beyond
+ *                 max_pages * page_size as that)
+ *   refs        : device, int32 [num_pages]: how many rows hold the page; a
+ *                 page with a count of 0 or less is free
+ *
+ * The tables, lengths and counts are read and written by the kernels, so
+ * every step can be enqueued, or captured in a CUDA graph, without the host
+ * knowing them. All pointers to 32-bit values are 4-byte aligned, pools and
+ * row data 16-byte aligned. The first call on a device allocates its status
+ * word (see attn_sync_status): make it before any stream capture.
+ */
+
+/*
+ * attn_decode_paged - attention of each sequence's T newest tokens over its
+ * paged keys and values.
+ *
+ * Sequence b holds lens[b] tokens, the T new ones (T >= 1) among them and
+ * already written. Token u, at position t_u = lens[b] - T + u, attends to the
+ * positions max(0, t_u - window) .. t_u (window < 0: 0 .. t_u) whose table
+ * entry is a page:
+ *
+ *   O[b,h,u]   = softmax(scale * q[b,h,u] . k) v   over those positions,
+ *   LSE[b,h,u] = ln sum exp(scale * q[b,h,u] . k)  (natural-log units),
+ *
+ * with key/value head h / (H / Hkv). A token with no such position (t_u < 0,
+ * or no page) gets O = 0 and LSE = -infinity.
+ *
+ *   q                : device, bf16 [B, H, T, d]
+ *   k_pages, v_pages : device, the pools, read only (see "Paged caches")
+ *   page_table, lens : device, int32 [B, max_pages] and [B], one row a sequence
+ *   o, lse           : device, bf16 [B, H, T, d] and fp32 [B, H, T], written
+ *   workspace        : device scratch owned by the caller, 16-byte aligned, at
+ *                      least attn_decode_paged_workspace_bytes(...) bytes. Its
+ *                      contents on entry do not matter; calls that may run at
+ *                      the same time need one each
+ *   page_size        : a power of two, 8 or more; max_pages * page_size at
+ *                      most 2^30; H / Hkv * T at most 256; d 64 or 128; others
+ *                      give ATTN_ERR_UNSUPPORTED
+ *
+ * Slots at or beyond lens[b], and slots no token's window reaches, may hold
+ * any bits, NaN included. Arithmetic as attn_decode; results are identical
+ * from run to run. Returns as attn_fwd.
+ */
+ATTN_API int attn_decode_paged(const void *q, const void *k_pages, const void *v_pages,
+                               const int64_t *kv_strides, const int *page_table, const int *lens,
+                               void *o, float *lse, void *workspace, size_t workspace_bytes, int B,
+                               int H, int Hkv, int T, int num_pages, int page_size, int max_pages,
+                               int window, int d, float scale, void *stream);
+
+/* Device workspace bytes attn_decode_paged needs, or -1 if the arguments are
+ * invalid or unsupported. */
+ATTN_API int64_t attn_decode_paged_workspace_bytes(int B, int H, int Hkv, int T, int max_pages,
+                                                   int page_size, int d);
+
+/*
+ * attn_decode_latent - attention of each sequence's T newest tokens over a
+ * paged cache of one latent vector a token, shared by all heads (latent
+ * attention in its absorbed form).
+ *
+ * A cached row c_j has rank + 64 elements: a latent vector, from which keys
+ * and values would be expanded, and the 64 elements of the shared positional
+ * key. With each head's expansion of the keys folded into its query and that
+ * of the values left to the caller's output projection, attention reads the
+ * cached rows as they are:
+ *
+ *   O[b,h,u]   = sum_j softmax_j(scale * q[b,h,u] . c_j) c_j[0 .. rank-1]
+ *   LSE[b,h,u] = ln sum_j exp(scale * q[b,h,u] . c_j)
+ *
+ * over the positions j = 0 .. lens[b] - T + u whose table entry is a page.
+ *
+ *   q       : device, bf16 [B, H, T, rank + 64]
+ *   pages   : device, the pool: [num_pages, page_size, rank + 64], or with
+ *             `strides` (host array of two, in elements, NULL: contiguous) the
+ *             strides between pages and tokens, multiples of 8
+ *   o, lse  : device, bf16 [B, H, T, rank] and fp32 [B, H, T], written
+ *   scale   : the expanded heads' own, which rank does not tell
+ *   rank    : 256 or 512; H * T at most 1024; page_size and max_pages as
+ *             attn_decode_paged; others give ATTN_ERR_UNSUPPORTED
+ * Everything else as attn_decode_paged.
+ */
+ATTN_API int attn_decode_latent(const void *q, const void *pages, const int64_t *strides,
+                                const int *page_table, const int *lens, void *o, float *lse,
+                                void *workspace, size_t workspace_bytes, int B, int H, int T,
+                                int num_pages, int page_size, int max_pages, int rank, float scale,
+                                void *stream);
+
+/* Device workspace bytes attn_decode_latent needs, or -1 if the arguments are
+ * invalid or unsupported. */
+ATTN_API int64_t attn_decode_latent_workspace_bytes(int B, int H, int T, int max_pages,
+                                                    int page_size, int rank);
+
+/*
+ * attn_pages_append - write new tokens' rows to their pages.
+ *
+ * New token u < count[b] of sequence b goes to position pos[b] + u. A position
+ * below 0, at or beyond max_pages * page_size, or whose table entry is no page
+ * is skipped.
+ *
+ *   k, v               : device, bf16 [B, Hkv, T, d], or with `k_strides`,
+ *                        `v_strides` (host arrays, may be NULL: contiguous)
+ *                        the strides in elements between sequences, heads and
+ *                        tokens, multiples of 8
+ *   k_pages, v_pages   : device, the pools, written
+ *   page_table, pos    : device, int32 [B, max_pages] and [B]
+ *   count              : device, int32 [B] clipped to 0 .. T, or NULL: T each
+ *   v = v_pages = NULL : a pool of latent rows (Hkv 1, d = rank + 64)
+ *   d                  : a multiple of 8 up to 1024, for all entry points
+ *                        below; num_pages at most 2^21 - 1; any page_size.
+ *                        Others give ATTN_ERR_UNSUPPORTED
+ * Two tokens of one call must not go to the same slot. Returns as attn_fwd.
+ */
+ATTN_API int attn_pages_append(const void *k, const void *v, const int64_t *k_strides,
+                               const int64_t *v_strides, void *k_pages, void *v_pages,
+                               const int64_t *kv_strides, const int *page_table, const int *pos,
+                               const int *count, int B, int Hkv, int T, int num_pages,
+                               int page_size, int max_pages, int d, void *stream);
+
+/* Device workspace bytes of attn_pages_reserve and attn_pages_fork for n
+ * requests, and (n = 0) of attn_pages_compact; -1 on bad input. */
+ATTN_API int64_t attn_pages_workspace_bytes(int n, int num_rows, int num_pages);
+
+/*
+ * attn_pages_reserve - give rows the pages their next tokens need.
+ *
+ * Request i fills the entries of row rows[i] that lie below
+ * ceil(want[i] / page_size) and hold no page with free pages, whose counts
+ * become 1. Requests are met in order, with the lowest free pages first, as
+ * long as the free pages suffice for all up to them; each is met in full or
+ * not at all. granted[i] becomes 1, or 0 where the pages did not suffice, the
+ * row is out of range or named by an earlier request, or want[i] exceeds
+ * max_pages * page_size; the row is left as it was then.
+ *
+ *   page_table, refs       : device, int32 [num_rows, max_pages], [num_pages]
+ *   rows, want, granted    : device, int32 [n]
+ *   workspace              : device, 4-byte aligned, at least
+ *                            attn_pages_workspace_bytes(n, num_rows, num_pages)
+ */
+ATTN_API int attn_pages_reserve(int *page_table, int *refs, const int *rows, const int *want,
+                                int *granted, void *workspace, size_t workspace_bytes, int n,
+                                int num_rows, int num_pages, int page_size, int max_pages,
+                                void *stream);
+
+/*
+ * attn_pages_fork - let new rows continue old ones.
+ *
+ * Request i makes row children[i], which must be empty (length 0 and no page
+ * in its first entry), a copy of row parents[i] as it was before the call: it
+ * shares the parent's full pages (their counts rise by 1) and gets a page of
+ * its own, the lowest free one, for the tokens of a last page that is not
+ * full; their rows are copied in every pool, the slots behind them are left
+ * as they were. Its other entries become -1. A call takes free pages in the
+ * order of its requests. granted[i] becomes 1, or 0 (child left as it was)
+ * where no free page is left, a row is out of range, the child is not empty or
+ * is named by an earlier request; fresh[i] is the page taken, or -1.
+ *
+ *   k_pages, v_pages  : device, the pools (v_pages NULL: one pool)
+ *   lens              : device, int32 [num_rows]; others as above
+ */
+ATTN_API int attn_pages_fork(void *k_pages, void *v_pages, const int64_t *kv_strides,
+                             int *page_table, int *lens, int *refs, const int *parents,
+                             const int *children, int *fresh, int *granted, void *workspace,
+                             size_t workspace_bytes, int n, int num_rows, int Hkv, int num_pages,
+                             int page_size, int max_pages, int d, void *stream);
+
+/*
+ * attn_pages_free - empty rows: the counts of the pages that rows[i] holds
+ * fall by 1, its entries become -1 and its length 0. A row named twice is
+ * emptied once; a row out of range is skipped.
+ */
+ATTN_API int attn_pages_free(int *page_table, int *lens, int *refs, const int *rows, int n,
+                             int num_rows, int num_pages, int max_pages, void *stream);
+
+/*
+ * attn_pages_compact - move the live pages to the front of the pools.
+ *
+ * With L pages live (count above 0), the live pages at L or above move, in
+ * ascending order, into the free pages below L in ascending order; all others
+ * stay. table_out is page_table with the moved pages' new numbers, refs_out
+ * the counts in their new places (0 for every free page), *live = L. The pages'
+ * old places keep their contents.
+ *
+ *   table_out, refs_out : device, int32, shaped as page_table and refs; each
+ *                         may be the input itself, else they must not overlap
+ *   live                : device, int32, written
+ */
+ATTN_API int attn_pages_compact(void *k_pages, void *v_pages, const int64_t *kv_strides,
+                                const int *page_table, const int *refs, int *table_out,
+                                int *refs_out, int *live, void *workspace, size_t workspace_bytes,
+                                int num_rows, int Hkv, int num_pages, int page_size, int max_pages,
+                                int d, void *stream);
 
 /*
  * attn_sync_status - synchronize `stream`, then read and clear this device's
