@@ -415,9 +415,10 @@ def _pools(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor]):
     """(Hkv, num_pages, page_size, d, strides) of one or two pools."""
     _check_pool("k_pages", k_pages)
     if v_pages is None:
-        if k_pages.dim() != 3:
-            raise ValueError("a pool of latent rows must be [num_pages, page_size, d]")
-        k_pages = k_pages.unsqueeze(1)
+        if k_pages.dim() == 3:
+            k_pages = k_pages.unsqueeze(1)
+        if k_pages.dim() != 4:
+            raise ValueError("a single pool must be [num_pages, page_size, d] or [num_pages, Hkv, page_size, d]")
     else:
         _check_pool("v_pages", v_pages)
         if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.device != v_pages.device:
@@ -522,7 +523,9 @@ def attn_decode_latent(q: torch.Tensor, pages: torch.Tensor, page_table: torch.T
     of a row are the values of every head. ``scale`` is the expanded heads' own
     (rank does not tell it). Returns (o [B, H, T, rank] or [B, H, rank], lse
     fp32). See include/attn.h."""
-    _, P, page, D, strides = _pools(pages, None)
+    Hkv, P, page, D, strides = _pools(pages, None)
+    if Hkv != 1:
+        raise ValueError("pages must be [num_pages, page_size, rank + 64]")
     if q.dtype != torch.bfloat16 or q.device != pages.device or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 tensor on the pages' device")
     if q.dim() not in (3, 4) or q.shape[-1] != D or D <= 64:
@@ -555,8 +558,9 @@ def pages_append(k: torch.Tensor, v: Optional[torch.Tensor], k_pages: torch.Tens
     """Write new tokens' rows to their pages, in place.
 
     k, v: bf16 [B, Hkv, T, d] of any strides whose last is 1; token u < count[b]
-    (default T) goes to position pos[b] + u. A pool of latent rows
-    [num_pages, page_size, d] takes k [B, 1, T, d] and v = v_pages = None.
+    (default T) goes to position pos[b] + u. A single pool, [num_pages,
+    page_size, d] (latent rows: k [B, 1, T, d]) or with heads as above, has
+    v = v_pages = None.
     page_table int32 [B, max_pages], pos and count int32 [B]."""
     if (v is None) != (v_pages is None):
         raise ValueError("v and v_pages go together")

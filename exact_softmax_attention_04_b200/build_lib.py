@@ -17,6 +17,7 @@ SOURCES = [os.path.join(CSRC, f) for f in ("attn_api.cu", "attn_bwd_api.cu", "at
                                              "attn_paged_api.cu", "attn_pages_api.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("attn_fwd_kernel.cuh", "attn_bwd_kernel.cuh",
                                             "attn_bwd_fused_kernel.cuh", "attn_decode_kernel.cuh",
+                                            "attn_paged_plan.cuh", "attn_paged_kernel.cuh",
                                             "attn_paged_simple.cuh", "attn_pages_kernel.cuh", "sm100.cuh",
                                             "attn_host.h")] + [
     os.path.join(ROOT, "include", "attn.h")]

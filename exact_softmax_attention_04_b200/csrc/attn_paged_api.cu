@@ -6,9 +6,11 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "attn.h"
 #include "attn_host.h"
+#include "attn_paged_kernel.cuh"
 #include "attn_paged_simple.cuh"
 
 namespace {
@@ -22,8 +24,9 @@ int check_cache(int B, int T, int num_pages, int page_size, int max_pages, float
     if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID;
     // a tile of the kernels is a whole number of pages, or lies inside one
     if (page_size < 8 || (page_size & (page_size - 1)) != 0) return ATTN_ERR_UNSUPPORTED;
-    // positions are 32-bit
-    if (static_cast<int64_t>(max_pages) * page_size > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+    // positions, and the tiles of all sequences, are counted in 32 bits
+    const int64_t cap = static_cast<int64_t>(max_pages) * page_size;
+    if (cap > (1 << 30) || cap > (int64_t(1) << 36) / B) return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }
 
@@ -34,7 +37,7 @@ int check_paged(int B, int H, int Hkv, int T, int num_pages, int page_size, int 
     if (H <= 0 || Hkv <= 0 || d <= 0 || H % Hkv != 0) return ATTN_ERR_INVALID;
     if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(B) * H > INT_MAX / T / d) return ATTN_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(H / Hkv) * T > 256) return ATTN_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(H / Hkv) * T > 256 || Hkv > 4096) return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }
 
@@ -61,6 +64,166 @@ int take_strides(const int64_t *given, int64_t Hkv, int64_t page_size, int64_t d
     return ATTN_OK;
 }
 
+// ---------------------------------------------------------------- the split
+
+constexpr int kSMs = 148;
+
+// How the work is laid out on the device: `ranges` runs of tiles for each of
+// `units` (heads or blocks of heads), and the workspace that takes.
+struct Layout {
+    int ranges, units;
+    int64_t before, ml, o, bytes;  // workspace offsets
+};
+
+// Runs per unit: whole waves of resident blocks cost alike whatever they hold,
+// so take the number that leaves the least per block times waves, the smaller
+// one of equals (it has fewer segments to join). There are no more runs than
+// tiles.
+Layout make_layout(int B, int units, int64_t max_tiles, int resident, int nc, int dv)
+{
+    Layout l;
+    l.units = units;
+    int64_t best = 1, best_waves = 0;
+    for (int64_t r = 1; r <= max_tiles && (r == 1 || (r - 1) * units <= 2 * resident); ++r) {
+        const int64_t waves = (r * units + resident - 1) / resident;
+        if (best_waves == 0 || waves * best < best_waves * r) {
+            best = r;
+            best_waves = waves;
+        }
+    }
+    l.ranges = static_cast<int>(best);
+    const int64_t cols = static_cast<int64_t>(l.ranges) * units * 2 * nc;
+    l.before = 0;
+    l.ml = B > attn_sm100::COMBINE_SCAN ? (static_cast<int64_t>(B) * 4 + 4 + 15) / 16 * 16 : 0;
+    l.o = l.ml + cols * 8;
+    l.bytes = l.o + cols * dv * 4;
+    return l;
+}
+
+// The joining kernel, which starts while the one before still runs and waits
+// for it.
+template <int TK, int DV, int DC, int NC>
+int launch_combine(const attn_sm100::PagedCombine &a, int rows, cudaStream_t st)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows), DV / DC);
+    cfg.blockDim = dim3(attn_sm100::COMBINE_THREADS);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_sm100::attn_paged_combine_kernel<TK, DV, DC, NC>, a) == cudaSuccess
+               ? ATTN_OK
+               : ATTN_ERR_CUDA;
+}
+
+// Rows of `cols` elements, boxes of 64 columns x `box_rows`.
+bool encode_rows(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, const void *ptr, int64_t rows, int cols,
+                 int box_rows)
+{
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A pool as [page][head][token][column], boxes of 64 columns x `box_rows`
+// tokens. Strides (page, head, token) in elements.
+bool encode_pool(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, const void *ptr, int64_t num_pages,
+                 int heads, int page_size, int cols, const int64_t s[3], int box_rows)
+{
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(page_size),
+                                static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(num_pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(s[2]) * 2, static_cast<cuuint64_t>(s[1]) * 2,
+                                   static_cast<cuuint64_t>(s[0]) * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int log2_of(int x)
+{
+    int n = 0;
+    while ((1 << n) < x) ++n;
+    return n;
+}
+
+// -------------------------------------------------------- keys and values
+
+// Columns a block handles: a group's G * T, rounded up.
+int paged_columns(int gt) { return gt <= 4 ? 4 : gt <= 8 ? 8 : gt <= 16 ? 16 : 32; }
+
+Layout paged_layout(int B, int H, int Hkv, int T, int max_pages, int page_size, int d)
+{
+    const int gt = H / Hkv * T, nc = paged_columns(gt);
+    const int64_t cap = static_cast<int64_t>(max_pages) * page_size;
+    const int64_t tiles = B * ((cap + attn_sm100::PAGED_TK - 1) / attn_sm100::PAGED_TK);
+    return make_layout(B, Hkv * ((gt + nc - 1) / nc), tiles, kSMs * (nc == 32 ? 1 : 2), nc, d);
+}
+
+struct PagedCall {
+    const void *q, *k, *v;
+    int64_t s[3];
+    attn_sm100::PagedParams p;
+    Layout l;
+    uint8_t *workspace;
+    int dev, page_size;
+    cudaStream_t st;
+};
+
+template <int D, int NC>
+int launch_paged(PagedCall &a)
+{
+    using C = attn_sm100::PagedCfg<D, NC>;
+    static bool set[kMaxDevices] = {};
+    auto enc = encoder();
+    if (!enc) return ATTN_ERR_CUDA;
+    attn_sm100::PagedParams &p = a.p;
+    CUtensorMap mq, mk, mv;
+    const int rows = p.split.B * p.H * p.split.T, box = a.page_size < 128 ? a.page_size : 128;
+    if (!encode_rows(enc, &mq, a.q, rows, D, C::N) ||
+        !encode_pool(enc, &mk, a.k, p.num_pages, p.Hkv, a.page_size, D, a.s, box) ||
+        !encode_pool(enc, &mv, a.v, p.num_pages, p.Hkv, a.page_size, D, a.s, box))
+        return ATTN_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!set[a.dev]) {
+            if (cudaFuncSetAttribute(attn_sm100::attn_paged_kernel<D, NC>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
+                return ATTN_ERR_CUDA;
+            set[a.dev] = true;
+        }
+    }
+    p.nblk = a.l.units / p.Hkv;
+    p.split.ranges = a.l.ranges;
+    p.split.before = reinterpret_cast<int *>(a.workspace + a.l.before);
+    p.part_ml = reinterpret_cast<float2 *>(a.workspace + a.l.ml);
+    p.part_o = reinterpret_cast<float *>(a.workspace + a.l.o);
+    const dim3 grid(static_cast<unsigned>(a.l.ranges), static_cast<unsigned>(a.l.units));
+    attn_sm100::attn_paged_kernel<D, NC><<<grid, attn_sm100::PAGED_THREADS, C::SMEM_BYTES, a.st>>>(mq, mk, mv, p);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+    // a sequence of one tile is never split
+    if (p.split.cap <= attn_sm100::PAGED_TK) return ATTN_OK;
+    const attn_sm100::PagedCombine c = {p.split, p.part_o, p.part_ml, p.o, p.lse, p.H, p.Hkv, p.nblk};
+    return launch_combine<attn_sm100::PAGED_TK, D, D, NC>(c, rows, a.st);
+}
+
+template <int D>
+int launch_paged_nc(PagedCall &a, int nc)
+{
+    if (nc == 4) return launch_paged<D, 4>(a);
+    if (nc == 8) return launch_paged<D, 8>(a);
+    if (nc == 16) return launch_paged<D, 16>(a);
+    return launch_paged<D, 32>(a);
+}
+
 int launch_simple(attn_sm100::PagedSimpleParams &p, int rows, cudaStream_t st)
 {
     attn_sm100::attn_paged_simple_kernel<<<static_cast<unsigned>(rows), attn_sm100::SIMPLE_THREADS, 0, st>>>(p);
@@ -73,7 +236,7 @@ extern "C" int64_t attn_decode_paged_workspace_bytes(int B, int H, int Hkv, int 
                                                      int d)
 {
     if (check_paged(B, H, Hkv, T, 1, page_size, max_pages, d, 1.f) != ATTN_OK) return -1;
-    return 16;
+    return paged_layout(B, H, Hkv, T, max_pages, page_size, d).bytes;
 }
 
 extern "C" int attn_decode_paged(const void *q, const void *k_pages, const void *v_pages, const int64_t *kv_strides,
@@ -89,12 +252,33 @@ extern "C" int attn_decode_paged(const void *q, const void *k_pages, const void 
     if (!aligned(page_table, 4) || !aligned(lens, 4) || !aligned(lse, 4)) return ATTN_ERR_INVALID;
     int64_t s[3];
     if (take_strides(kv_strides, Hkv, page_size, d, s) != ATTN_OK) return ATTN_ERR_INVALID;
-    if (workspace_bytes < 16) return ATTN_ERR_INVALID;
-    attn_sm100::PagedSimpleParams p = {
-        static_cast<const __nv_bfloat16 *>(q), static_cast<const __nv_bfloat16 *>(k_pages),
-        static_cast<const __nv_bfloat16 *>(v_pages), s[0], s[1], s[2], page_table, lens,
-        static_cast<__nv_bfloat16 *>(o), lse, H, Hkv, T, num_pages, page_size, max_pages, window, d, d, scale};
-    return launch_simple(p, B * H * T, static_cast<cudaStream_t>(stream));
+    PagedCall a;
+    a.l = paged_layout(B, H, Hkv, T, max_pages, page_size, d);
+    if (workspace_bytes < static_cast<size_t>(a.l.bytes)) return ATTN_ERR_INVALID;
+    if (current_device(&a.dev) != ATTN_OK) return ATTN_ERR_CUDA;
+    attn_sm100::PagedParams &p = a.p;
+    p.status = status_word(a.dev);
+    if (!p.status) return ATTN_ERR_CUDA;
+    a.q = q;
+    a.k = k_pages;
+    a.v = v_pages;
+    for (int i = 0; i < 3; ++i) a.s[i] = s[i];
+    a.workspace = static_cast<uint8_t *>(workspace);
+    a.page_size = page_size;
+    a.st = static_cast<cudaStream_t>(stream);
+    // (a window past every position is none; kept small, it cannot overflow)
+    p.split = {lens, B, T, max_pages * page_size, window < 0 || window >= (1 << 30) ? -1 : window, 0, nullptr};
+    p.table = page_table;
+    p.o = static_cast<__nv_bfloat16 *>(o);
+    p.lse = lse;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.num_pages = num_pages;
+    p.max_pages = max_pages;
+    p.page_log2 = log2_of(page_size);
+    p.scale_log2 = scale * 1.4426950408889634f;
+    const int nc = paged_columns(H / Hkv * T);
+    return d == 64 ? launch_paged_nc<64>(a, nc) : launch_paged_nc<128>(a, nc);
 }
 
 extern "C" int64_t attn_decode_latent_workspace_bytes(int B, int H, int T, int max_pages, int page_size, int rank)

@@ -1,0 +1,257 @@
+// attn_paged_plan.cuh - how the work of attention over a paged cache is split,
+// and how the parts are joined. Shared by the kernels for pages of keys and
+// values and for pages of latent vectors.
+//
+// The positions a sequence's new tokens see are cut into tiles of TK; the
+// tiles of all sequences, in order, are dealt out as `ranges` contiguous runs
+// that differ by one tile at most, one to each block of the grid's x (the y
+// blocks take the heads of the same run). So every block has the same amount
+// to read whatever the lengths are, and the host need not know them. Within a
+// run, the tiles of one sequence are a segment. A segment that is the whole
+// sequence is finished by its block. Others leave their unnormalised O, maximum
+// and sum in the workspace: a block has two such segments at most, its first
+// and its last, so it has two places there; `attn_paged_combine_kernel` joins
+// them. A sequence without a position counts as one tile, so that its (empty)
+// answer is written like any other.
+#pragma once
+#include "attn_fwd_kernel.cuh"
+
+namespace attn_sm100 {
+
+struct PagedSplit {
+    const int *lens;      // [B]
+    int B, T, cap;        // cap: positions that the table holds
+    int window;           // -1: none
+    int ranges;           // gridDim.x
+    int *before;          // workspace [B + 1]: tiles before each sequence, then all (B > COMBINE_SCAN)
+};
+
+// Up to this many sequences, the joining kernel sums their tiles itself, while
+// the kernel before it still runs; with more it reads what block (0, 0) wrote.
+constexpr int COMBINE_SCAN = 1024;
+
+// The tiles of one sequence: positions first * TK up to len - 1.
+struct PagedSeq {
+    int len, first, ntiles;
+};
+
+template <int TK>
+__device__ __forceinline__ PagedSeq paged_seq(const PagedSplit &p, int b)
+{
+    PagedSeq s;
+    s.len = min(max(__ldg(p.lens + b), 0), p.cap);
+    s.first = p.window >= 0 ? max(0, s.len - p.T - p.window) / TK : 0;
+    s.ntiles = max(s.len - 1, 0) / TK - s.first + 1;
+    return s;
+}
+
+// First tile of run r out of n = min(ranges, total).
+__device__ __forceinline__ int paged_run_start(int total, int r, int n)
+{
+    return static_cast<int>(static_cast<int64_t>(total) * r / n);
+}
+
+// A place in the order of all tiles: tile j of sequence b.
+template <int TK>
+struct PagedWalk {
+    int b, j;
+    PagedSeq s;
+
+    __device__ __forceinline__ void start(const PagedSplit &p, int b0, int j0)
+    {
+        b = b0;
+        j = j0;
+        s = paged_seq<TK>(p, b0);
+    }
+    // (the caller does not step past the last tile)
+    __device__ __forceinline__ void step(const PagedSplit &p)
+    {
+        if (++j == s.ntiles) start(p, b + 1, 0);
+    }
+    __device__ __forceinline__ int base() const { return (s.first + j) * TK; }
+    __device__ __forceinline__ bool last() const { return j + 1 == s.ntiles; }
+};
+
+struct PagedRun {
+    int b, j, count;  // first tile, number of tiles (0: none)
+};
+
+// The block's run, for all its NT threads.
+template <int TK, int NT>
+__device__ __forceinline__ PagedRun paged_run(const PagedSplit &p, int r)
+{
+    __shared__ int sums[NT / 32];
+    __shared__ PagedRun run;
+    const int tid = threadIdx.x, lane = tid % 32;
+    const int per = (p.B + NT - 1) / NT;
+    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) mine += paged_seq<TK>(p, b).ntiles;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int t = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += t;
+    }
+    if (lane == 31) sums[tid / 32] = upto;
+    if (tid == 0) run.count = 0;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < tid / 32) upto += sums[w];
+        total += sums[w];
+    }
+    if (p.B > COMBINE_SCAN && blockIdx.x == 0 && blockIdx.y == 0) {
+        int at = upto - mine;
+        for (int b = b0; b < b1; ++b) {
+            p.before[b] = at;
+            at += paged_seq<TK>(p, b).ntiles;
+        }
+        if (tid == 0) p.before[p.B] = total;
+    }
+    const int n = min(p.ranges, total);
+    if (r < n) {
+        const int t0 = paged_run_start(total, r, n);
+        int at = upto - mine;
+        if (t0 >= at && t0 < upto) {
+            for (int b = b0; b < b1; ++b) {
+                const int tiles = paged_seq<TK>(p, b).ntiles;
+                if (t0 < at + tiles) {
+                    run.b = b;
+                    run.j = t0 - at;
+                    run.count = paged_run_start(total, r + 1, n) - t0;
+                    break;
+                }
+                at += tiles;
+            }
+        }
+    }
+    __syncthreads();
+    return run;
+}
+
+// The segments' results in the workspace: for slot s (two for each block: x,
+// then y, then which) and column c of NC, O at o[(s * NC + c) * DV] and the
+// maximum (log2 units) and sum at ml[s * NC + c].
+__device__ __forceinline__ int64_t paged_slot(int x, int y, int ranges, bool first)
+{
+    return (static_cast<int64_t>(y) * ranges + x) * 2 + (first ? 0 : 1);
+}
+
+struct PagedCombine {
+    PagedSplit split;
+    const float *part_o;
+    const float2 *part_ml;
+    __nv_bfloat16 *o;  // [B, H, T, DV]
+    float *lse;        // [B, H, T]
+    int H, Hkv, nblk;  // heads; column blocks of a group
+};
+
+constexpr int COMBINE_THREADS = 256;
+
+// Joins the segments of one query row (grid x), DC of its DV columns (grid y):
+//   M = max_s m_s, l = sum_s l_s 2^(m_s - M), O = sum_s O_s 2^(m_s - M) / l.
+// DC / 4 lanes take 16 bytes each of a segment, and the groups of lanes take
+// the segments in turn, so that a hundred segments of a long sequence are a
+// dozen loads deep. Which segments there are follows from the lengths alone
+// and is worked out while the kernel before is still running.
+template <int TK, int DV, int DC, int NC>
+__global__ void __launch_bounds__(COMBINE_THREADS) attn_paged_combine_kernel(const PagedCombine a)
+{
+    constexpr int LANES = DC / 4, GROUPS = COMBINE_THREADS / LANES;
+    __shared__ int red[2][COMBINE_THREADS / 32];
+    __shared__ float4 acc_s[GROUPS][LANES];
+    __shared__ float l_s[GROUPS];
+    const PagedSplit &p = a.split;
+    const int row = blockIdx.x, tid = threadIdx.x;
+    const int G = a.H / a.Hkv, GT = G * p.T;
+    const int unit = row / GT;  // b * Hkv + key/value head
+    const int b = unit / a.Hkv, gc = row % GT;
+    const int y = (unit % a.Hkv) * a.nblk + gc / NC, c = gc % NC;
+
+    int before = 0, total = 0;
+    if (p.B <= COMBINE_SCAN) {
+        for (int i = tid; i < p.B; i += COMBINE_THREADS) {
+            const int n = paged_seq<TK>(p, i).ntiles;
+            total += n;
+            before += i < b ? n : 0;
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o /= 2) {
+            total += __shfl_xor_sync(0xffffffffu, total, o);
+            before += __shfl_xor_sync(0xffffffffu, before, o);
+        }
+        if (tid % 32 == 0) {
+            red[0][tid / 32] = total;
+            red[1][tid / 32] = before;
+        }
+        __syncthreads();
+        total = before = 0;
+#pragma unroll
+        for (int w = 0; w < COMBINE_THREADS / 32; ++w) {
+            total += red[0][w];
+            before += red[1][w];
+        }
+    } else {
+        grid_dependency_wait();
+        before = p.before[b];
+        total = p.before[p.B];
+    }
+    const int end = before + paged_seq<TK>(p, b).ntiles - 1;  // the last tile
+    const int n = min(p.ranges, total);
+    // the runs that hold the first and the last tile
+    const int r0 = static_cast<int>(((static_cast<int64_t>(before) + 1) * n - 1) / total);
+    const int r1 = static_cast<int>(((static_cast<int64_t>(end) + 1) * n - 1) / total);
+    const int nseg = r1 - r0 + 1;
+    // run r0 may begin before the sequence; then this is its last segment
+    const bool r0_first = paged_run_start(total, r0, n) >= before;
+    auto slot = [&](int s) { return paged_slot(r0 + s, y, p.ranges, s > 0 || r0_first) * NC + c; };
+
+    grid_dependency_wait();
+    if (r0 == r1) return;  // one block had the whole sequence
+
+    float M = -CUDART_INF_F;
+    for (int s = tid % 32; s < nseg; s += 32) M = fmaxf(M, a.part_ml[slot(s)].x);
+    M = redux_max(M);
+    const float ref = M == -CUDART_INF_F ? 0.f : M;
+    const int g = tid / LANES, e = tid % LANES;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int s = g; s < nseg; s += GROUPS) {
+        const int64_t at = slot(s);
+        const float2 ml = a.part_ml[at];
+        const float4 v = *reinterpret_cast<const float4 *>(a.part_o + at * DV + blockIdx.y * DC + 4 * e);
+        const float f = ex2_approx(ml.x - ref);  // 0 for a segment without a position
+        l = fmaf(ml.y, f, l);
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
+    }
+    acc_s[g][e] = acc;
+    if (e == 0) l_s[g] = l;
+    __syncthreads();
+    if (g != 0) return;
+#pragma unroll
+    for (int i = 1; i < GROUPS; ++i) {
+        const float4 v = acc_s[i][e];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+        l += l_s[i];
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    uint2 w;
+    w.x = *reinterpret_cast<const uint32_t *>(&lo);
+    w.y = *reinterpret_cast<const uint32_t *>(&hi);
+    *reinterpret_cast<uint2 *>(a.o + static_cast<int64_t>(row) * DV + blockIdx.y * DC + 4 * e) = w;
+    if (e == 0 && blockIdx.y == 0)
+        a.lse[row] = l == 0.f ? -CUDART_INF_F : (M + __log2f(l)) * 0.69314718055994531f;
+}
+
+}  // namespace attn_sm100

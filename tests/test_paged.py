@@ -191,6 +191,11 @@ def test_paged_many_short_sequences(gpu):
 
 
 @pytest.mark.gpu
+def test_paged_more_sequences_than_one_block_sums(gpu):
+    paged_case(gpu, 1, 4, 1, 64, 16, [(i * 83) % 600 for i in range(1500)], seed=6)
+
+
+@pytest.mark.gpu
 def test_paged_large_logits(gpu):
     paged_case(gpu, 2, 4, 1, 128, 16, [5, 400, 3000], seed=9, std=12.0)
 
