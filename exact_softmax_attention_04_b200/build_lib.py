@@ -18,7 +18,7 @@ SOURCES = [os.path.join(CSRC, f) for f in ("attn_api.cu", "attn_bwd_api.cu", "at
 HEADERS = [os.path.join(CSRC, f) for f in ("attn_fwd_kernel.cuh", "attn_bwd_kernel.cuh",
                                             "attn_bwd_fused_kernel.cuh", "attn_decode_kernel.cuh",
                                             "attn_paged_plan.cuh", "attn_paged_kernel.cuh",
-                                            "attn_paged_simple.cuh", "attn_pages_kernel.cuh", "sm100.cuh",
+                                            "attn_latent_kernel.cuh", "attn_pages_kernel.cuh", "sm100.cuh",
                                             "attn_host.h")] + [
     os.path.join(ROOT, "include", "attn.h")]
 

@@ -1,0 +1,551 @@
+// attn_latent_kernel.cuh - attention of each sequence's newest tokens over
+// pages of latent vectors, shared by all heads.
+//
+// A row of the cache, R + 64 elements, is the key of every head and its first R
+// elements are the value. The H * T query rows of a sequence are the columns
+// of (tile: 64 positions, C its rows)
+//   S^T  = C q^T            M = 64 positions, K = R + 64: C K-major;
+//   O^T += C[:, :R]^T P^T   M = R, as blocks of 128, K = 64 positions: the same
+//                           bytes of shared memory as an MN-major operand,
+// so a tile is loaded once and used twice: up to 242 operations a byte at 128
+// heads, where the tensor cores' rate and the memory's are both near. What
+// bounds a block is shared memory: a product reads 2 to 4 KB of C per
+// instruction whatever the number of columns. 64 columns a block is the most
+// that O^T (R x 64 in fp32: half of TMEM at R = 512), q (72 KB) and two tiles of
+// 72 KB leave room for; 128 heads are two blocks that read the same tiles at the
+// same time, the second out of L2.
+//
+// Roles as in attn_paged_kernel.cuh. With M = 64, S^T lies in the lower 16 lanes
+// of each quarter of TMEM; read as 8 x 8 blocks, all 32 threads of a warp get a
+// share of them, and P^T goes to shared memory by transposing stores. A thread
+// has 2 positions of NC / 4 columns; maxima over a tile go through three
+// shuffles and then between the four warps.
+#pragma once
+#include "attn_paged_plan.cuh"
+
+namespace attn_sm100 {
+
+struct LatentParams {
+    PagedSplit split;
+    PagedTable pages;
+    __nv_bfloat16 *o;         // [B, H, T, R]
+    float *lse;               // [B, H, T]
+    float *part_o;            // see paged_slot
+    float2 *part_ml;
+    int *status;
+    int GT;                   // query rows of a sequence, H * T
+    float scale_log2;         // scale * log2(e)
+};
+
+constexpr int LATENT_TK = 64;  // positions per tile
+constexpr int LATENT_THREADS = 192;
+constexpr float LATENT_SLACK = 8.f;  // as PAGED_SLACK
+
+template <int R, int NC>
+struct LatentCfg {
+    static_assert(R == 256 || R == 512, "rank 256 or 512");
+    static_assert(NC == 16 || NC == 32 || NC == 64, "columns");
+    static constexpr int BOXES = R / 64 + 1;                   // 64-column boxes per row
+    static constexpr int BLOCKS = R / 128;                     // blocks of O^T
+    static constexpr int BOX_BYTES_T = LATENT_TK * 128;        // [64 positions x 64 columns] bf16
+    static constexpr int TILE_BYTES = BOXES * BOX_BYTES_T;
+    static constexpr int OPB_BOX = NC * 128;                   // NC rows x 64 elements
+    static constexpr int Q_BYTES = BOXES * OPB_BOX;
+    static constexpr int P_BYTES = OPB_BOX;                    // NC rows x 64 positions
+    static constexpr int TAIL = 2 * 4 * NC * 4 + NC * 8 + 512; // what follows the operands, at most
+    static constexpr int NST = (232448 - Q_BYTES - P_BYTES - TAIL) / TILE_BYTES;
+    static constexpr int Q_OFF = NST * TILE_BYTES;
+    static constexpr int P_OFF = Q_OFF + Q_BYTES;
+    static constexpr int RED_OFF = P_OFF + P_BYTES;            // fp32 [2][4 warps][NC]
+    static constexpr int COL_OFF = RED_OFF + 2 * 4 * NC * 4;   // float2 [NC]: rescaling factor, maximum
+    static constexpr int BAR_OFF = COL_OFF + NC * 8;
+    // full[NST], empty[NST], s_full[2], s_free[2], q_full, q_empty, p_full, pv_done, mma_drain
+    static constexpr int NBAR = 2 * NST + 9;
+    static constexpr int PLAN_OFF = (BAR_OFF + NBAR * 8 + 15) / 16 * 16;
+    static constexpr int MISC_OFF = PLAN_OFF + PLAN_SCRATCH;   // TMEM base, abort flag
+    // (no slack for alignment: the kernel has no other shared memory, and
+    // checks that its base is a multiple of 1 KB)
+    static constexpr int SMEM_BYTES = MISC_OFF + 16;
+    static constexpr uint32_t O_COL = 2 * NC;                  // behind two S buffers
+    static constexpr uint32_t TMEM_NEED = 2 * NC + BLOCKS * NC;
+    static constexpr uint32_t TMEM_COLS = TMEM_NEED <= 128 ? 128 : TMEM_NEED <= 256 ? 256 : 512;
+    static_assert(NST >= 2 && SMEM_BYTES <= 232448, "shared memory");
+    static_assert(Q_OFF % 1024 == 0 && P_OFF % 1024 == 0, "operand alignment");
+};
+
+// Warp-uniform read of NC / 2 registers (see tmem_ld_half8).
+template <int NC>
+__device__ __forceinline__ void latent_ld_s(uint32_t taddr, uint32_t (&r)[NC / 2])
+{
+    if constexpr (NC == 16) {
+        tmem_ld_half8(taddr, r);
+    } else if constexpr (NC == 32) {
+        tmem_ld_half16(taddr, r);
+    } else {
+        tmem_ld_half32(taddr, r);
+    }
+}
+
+template <int W>
+__device__ __forceinline__ void latent_ld_o(uint32_t taddr, uint32_t (&r)[W])
+{
+    if constexpr (W == 16) {
+        tmem_ld16(taddr, r);
+    } else {
+        tmem_ld32(taddr, r);
+    }
+}
+
+template <int R, int NC>
+__global__ void __launch_bounds__(LATENT_THREADS, 1)
+    attn_latent_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
+                       const LatentParams p)
+{
+    using C = LatentCfg<R, NC>;
+    using Walk = PagedWalk<LATENT_TK>;
+    constexpr int NST = C::NST;
+    constexpr int NK = NC / 8;  // blocks of 8 columns
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t base = smem_addr(smem_raw);
+    auto ring = [&](int st) { return base + st * C::TILE_BYTES; };
+    const uint32_t sQ = base + C::Q_OFF, sP = base + C::P_OFF;
+    float *const red = reinterpret_cast<float *>(smem_raw + C::RED_OFF);
+    float2 *const col_s = reinterpret_cast<float2 *>(smem_raw + C::COL_OFF);
+    const uint32_t bars = base + C::BAR_OFF;
+    auto full = [&](int st) { return bars + 8u * st; };
+    auto empty = [&](int st) { return bars + 8u * (NST + st); };
+    auto bar1 = [&](int i) { return bars + 8u * (2 * NST + i); };
+    auto s_full = [&](int i) { return bar1(i); };
+    auto s_free = [&](int i) { return bar1(2 + i); };
+    const uint32_t q_full = bar1(4), q_empty = bar1(5), p_full = bar1(6), pv_done = bar1(7), mma_drain = bar1(8);
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + C::MISC_OFF);
+    volatile int *const abort_flag = reinterpret_cast<volatile int *>(smem_raw + C::MISC_OFF + 4);
+
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
+    const int lane = static_cast<int>(threadIdx.x % 32);
+    const int T = p.split.T;
+    const int c0 = blockIdx.y * NC;                  // first column of this block
+    const int ncol = min(p.GT - c0, NC);             // columns in use
+
+    grid_dependents_launch();
+    if (base % 1024 != 0) {
+        // (the operands' swizzle needs it)
+        if (threadIdx.x == 0) atomicOr(p.status, STATUS_WAIT_TIMEOUT);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmC);
+        for (int st = 0; st < NST; ++st) {
+            mbar_init(full(st), 1);
+            mbar_init(empty(st), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full(i), 1);
+            mbar_init(s_free(i), 4 * 32);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        mbar_init(p_full, 4 * 32);
+        mbar_init(pv_done, 1);
+        mbar_init(mma_drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_addr(tmem_slot), C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    // (synchronises the block)
+    const PagedRun run = paged_run<LATENT_TK, LATENT_THREADS>(p.split, blockIdx.x, smem_raw + C::PLAN_OFF);
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const Waiter wt{abort_flag, p.status};
+    const int count = run.count;
+
+    if (count == 0) {
+        // fewer tiles than blocks: nothing to do
+    } else if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        const uint32_t leader = elect_one();
+        const int page = 1 << p.pages.page_log2;
+        const int npg = max(1, LATENT_TK >> p.pages.page_log2);  // pages per tile, one per lane
+        const int rows = min(page, LATENT_TK);
+        Walk w;
+        w.start(p.split, run.b, run.j);
+        auto lane_page = [&]() {
+            const int at = w.base() + lane * page;
+            return lane < npg ? paged_page(p.split, p.pages, w.s, w.b, npg == 1 ? at & ~(page - 1) : at) : -1;
+        };
+        int id = lane_page();
+        int items = 0, segs = 0;
+        bool ok = true;
+        for (int i = 0; ok && i < count; ++i) {
+            const int cur = id, b = w.b;
+            const int row = npg == 1 ? w.base() & (page - 1) : 0;  // within the page
+            const bool starts = i == 0 || w.j == 0;
+            // the next tile's table entries travel while this one is issued
+            if (i + 1 < count) {
+                w.step(p.split);
+                id = lane_page();
+            }
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, cur >= 0)) * rows * (128 * C::BOXES);
+            const int st = items % NST;
+            if (items >= NST) ok = __all_sync(0xffffffffu, wt.wait(empty(st), ((items / NST) - 1) & 1u));
+            if (!ok) break;
+            if (leader) mbar_arrive_expect_tx(full(st), bytes);
+            __syncwarp();
+            if (cur >= 0) {
+                if (rows == LATENT_TK) {
+                    // one box of all the columns
+                    tma_load_4d(ring(st), &tmC, full(st), 0, row, 0, cur);
+                } else {
+                    for (int bx = 0; bx < C::BOXES; ++bx)
+                        tma_load_4d(ring(st) + bx * C::BOX_BYTES_T + lane * rows * 128, &tmC, full(st), 0, row, bx, cur);
+                }
+            }
+            __syncwarp();
+            ++items;
+            if (starts) {
+                if (segs >= 1) ok = __all_sync(0xffffffffu, wt.wait(q_empty, (segs - 1) & 1u));
+                if (!ok) break;
+                if (leader) {
+                    mbar_arrive_expect_tx(q_full, C::Q_BYTES);
+                    for (int bx = 0; bx < C::BOXES; ++bx)
+                        tma_load_2d(sQ + bx * C::OPB_BOX, &tmQ, q_full, bx * BOX_COLS, b * p.GT + c0);
+                }
+                ++segs;
+            }
+        }
+        // copies still in flight must land before the CTA exits
+        for (int st = 0; st < NST; ++st) {
+            if (items > st) wt.drain(full(st), ((items - 1 - st) / NST) & 1u);
+        }
+        if (segs > 0) wt.drain(q_full, (segs - 1) & 1u);
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        const uint32_t leader = elect_one();
+        constexpr uint32_t idesc_s = idesc_bf16_f32(LATENT_TK, NC, 0, 0);  // C, q both K-major
+        constexpr uint32_t idesc_o = idesc_bf16_f32(128, NC, 1, 0);        // C^T MN-major, P^T K-major
+        const uint64_t qdesc = smem_desc_sw128(sQ, 16, 1024);
+        const uint64_t pdesc = smem_desc_sw128(sP, 16, 1024);
+        Walk ws, wo;  // where the next scores and the next products are
+        ws.start(p.split, run.b, run.j);
+        wo = ws;
+        int segs = 0;  // segments whose q has been waited for
+        // Phases are tested one at a time and in order: a barrier is asked about
+        // a phase only when the one before it is known to have completed.
+        auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
+        auto s_ready = [&](int i) {
+            const bool starts = i == 0 || ws.j == 0;
+            // the softmax must have read S(i - 2) out of this buffer
+            return all(mbar_test_wait(full(i % NST), (i / NST) & 1u) &&
+                       (i < 2 || mbar_test_wait(s_free(i % 2), ((i - 2) / 2) & 1u)) &&
+                       (!starts || mbar_test_wait(q_full, segs & 1u)));
+        };
+        // S(i) = C_i q^T into S buffer i % 2
+        auto issue_s = [&](int i) {
+            if (i == 0 || ws.j == 0) ++segs;
+            tc_fence_after();
+            const uint64_t kdesc = smem_desc_sw128(ring(i % NST), 16, 1024);
+            const uint32_t d_col = tmem + NC * (i % 2);
+#pragma unroll
+            for (int k = 0; k < (R + 64) / 16; ++k) {
+                const uint64_t koff = static_cast<uint64_t>(((k / 4) * C::BOX_BYTES_T + (k % 4) * 32) >> 4);
+                const uint64_t qoff = static_cast<uint64_t>(((k / 4) * C::OPB_BOX + (k % 4) * 32) >> 4);
+                mma_bf16_ss_if(leader, d_col, kdesc + koff, qdesc + qoff, idesc_s, k > 0 ? 1u : 0u);
+            }
+            mma_commit_if(leader, s_full(i % 2));
+            if (ws.last()) mma_commit_if(leader, q_empty);
+            if (i + 1 < count) ws.step(p.split);
+        };
+        // O^T += C_i[:, :R]^T P_i^T; a segment's first tile starts from zero
+        auto issue_pv = [&](int i) {
+            tc_fence_after();
+            const uint32_t more = (i == 0 || wo.j == 0) ? 0u : 1u;
+            const uint64_t vdesc = smem_desc_sw128(ring(i % NST), C::BOX_BYTES_T, 1024);
+#pragma unroll
+            for (int blk = 0; blk < C::BLOCKS; ++blk) {
+#pragma unroll
+                for (int k = 0; k < LATENT_TK / 16; ++k)
+                    mma_bf16_ss_if(leader, tmem + C::O_COL + blk * NC,
+                                   vdesc + static_cast<uint64_t>(((2 * blk * C::BOX_BYTES_T) >> 4) + k * 128),
+                                   pdesc + static_cast<uint64_t>(k * 2), idesc_o, k > 0 ? 1u : more);
+            }
+            mma_commit_if(leader, pv_done);
+            mma_commit_if(leader, empty(i % NST));
+            if (i + 1 < count) wo.step(p.split);
+        };
+        // Whichever is ready: the next scores must not hold up the products,
+        // which free the tile that the load after next waits for.
+        int ns = 0, np = 0;
+        uint64_t since = 0;
+        for (uint32_t spins = 0; np < count; ++spins) {
+            bool did = false;
+            if (ns < count && ns <= np + 1 && s_ready(ns)) {
+                issue_s(ns++);
+                did = true;
+            }
+            if (np < ns && all(mbar_test_wait(p_full, np & 1u))) {
+                issue_pv(np++);
+                did = true;
+            }
+            if (did) {
+                since = 0;
+            } else if ((spins & 63u) == 0 || since == 0) {
+                // give up as Waiter::wait does
+                const uint64_t now = global_timer_ns();
+                if (since == 0) since = now;
+                const bool late = __any_sync(0xffffffffu, now - since > WAIT_LIMIT_NS);
+                if (__any_sync(0xffffffffu, late || *abort_flag)) {
+                    if (leader && late) {
+                        *abort_flag = 1;
+                        atomicOr(p.status, STATUS_WAIT_TIMEOUT);
+                    }
+                    break;
+                }
+            }
+        }
+        // every MMA this warp issued must finish before TMEM is freed
+        mma_commit_if(leader, mma_drain);
+        wt.drain(mma_drain, 0);
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int sw = warp % 4;                    // TMEM quarter: positions 16 sw + 0..15 of the tile
+        const int rank_lane = sw * 32 + lane;       // row of an O^T block
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(sw * 32) << 16);
+        const int cc = 2 * (lane % 4);              // this thread's columns: 8 k + cc, 8 k + cc + 1
+        const int rr = lane / 4;                    // its positions: 16 sw + rr and 8 further
+        const int my_row = 16 * sw + lane % 16;     // the position whose page this lane looks up
+        const float sc = p.scale_log2;
+        constexpr int OW = NC < 32 ? NC : 32;       // columns of O^T read at a time
+        Walk w;
+        w.start(p.split, run.b, run.j);
+        auto row_page = [&]() {
+            return paged_page(p.split, p.pages, w.s, w.b, (w.base() + my_row) & ~((1 << p.pages.page_log2) - 1));
+        };
+        int id = row_page();
+        float m_run[NC / 4], l_part[NC / 4];
+        bool ok = true;
+        int seg_j = run.j;  // where the segment began
+        for (int i = 0; i < count; ++i) {
+            const int sb = i % 2, st = i % NST;
+            const Walk cur = w;
+            const bool starts = i == 0 || cur.j == 0, ends = i + 1 == count || cur.last();
+            const int len = cur.s.len;
+            // Seen by a token at all, and by all of them? Bits by row of the
+            // warp's 16.
+            const bool seen = id >= 0 && cur.base() + my_row < len;
+            const uint32_t seen_rows = __ballot_sync(0xffffffffu, seen) & 0xffffu;
+            const bool plain = __all_sync(0xffffffffu, seen && cur.base() + my_row <= len - T);
+            if (i + 1 < count) {
+                w.step(p.split);
+                id = row_page();
+            }
+            if (starts) {
+#pragma unroll
+                for (int c = 0; c < NC / 4; ++c) {
+                    m_run[c] = -CUDART_INF_F;
+                    l_part[c] = 0.f;
+                }
+                seg_j = cur.j;
+            }
+            bool okw = __all_sync(0xffffffffu, wt.wait(s_full(sb), (i / 2) & 1u));
+            float s[NC / 2];  // [8-column block][position rr, rr + 8][column]
+            if (okw) {
+                tc_fence_after();
+                uint32_t sv[NC / 2];
+                latent_ld_s<NC>(lane_base + NC * sb, sv);
+                tc_fence_before();
+                mbar_arrive(s_free(sb));
+#pragma unroll
+                for (int e = 0; e < NC / 2; ++e) s[e] = __uint_as_float(sv[e]) * sc;
+                if (!plain) {
+#pragma unroll
+                    for (int e = 0; e < NC / 2; ++e) {
+                        const int row = rr + ((e & 2) ? 8 : 0), c = c0 + 8 * (e / 4) + cc + (e & 1);
+                        const int at = cur.base() + 16 * sw + row;
+                        const bool allowed = ((seen_rows >> row) & 1u) && at <= len - T + c % T;
+                        s[e] = allowed ? s[e] : -CUDART_INF_F;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < NK; ++k) {
+                    float a = fmaxf(s[4 * k], s[4 * k + 2]), b = fmaxf(s[4 * k + 1], s[4 * k + 3]);
+#pragma unroll
+                    for (int o = 4; o <= 16; o *= 2) {
+                        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+                        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+                    }
+                    if (lane < 4)
+                        *reinterpret_cast<float2 *>(red + (sb * 4 + sw) * NC + 8 * k + cc) = make_float2(a, b);
+                }
+            }
+            // (ok carries a wait that gave up later in the previous tile)
+            ok = named_bar_and(1, 4 * 32, okw && ok);
+            if (!ok) break;
+            float alpha[NC / 4];
+            bool raised = false;
+#pragma unroll
+            for (int k = 0; k < NK; ++k) {
+                float2 mx = *reinterpret_cast<const float2 *>(red + sb * 4 * NC + 8 * k + cc);
+#pragma unroll
+                for (int v = 1; v < 4; ++v) {
+                    const float2 t = *reinterpret_cast<const float2 *>(red + (sb * 4 + v) * NC + 8 * k + cc);
+                    mx.x = fmaxf(mx.x, t.x);
+                    mx.y = fmaxf(mx.y, t.y);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int c = 2 * k + e;
+                    const float tmax = e ? mx.y : mx.x;
+                    // (a column without a position so far has -inf)
+                    const bool up = tmax > m_run[c] + LATENT_SLACK;
+                    const float m_new = up ? tmax : m_run[c];
+                    // measure from 0 while there is none, so that no (-inf) - (-inf) arises
+                    const float m_ref = (m_new == -CUDART_INF_F) ? 0.f : m_new;
+                    alpha[c] = up ? ex2_approx(m_run[c] - m_ref) : 1.f;
+                    const float p0 = ex2_approx(s[4 * k + e] - m_ref), p1 = ex2_approx(s[4 * k + 2 + e] - m_ref);
+                    s[4 * k + e] = p0;
+                    s[4 * k + 2 + e] = p1;
+                    l_part[c] = fmaf(l_part[c], alpha[c], p0 + p1);
+                    m_run[c] = m_new;
+                    raised = raised || up;
+                }
+            }
+            // P^T was last read by PV(i - 1), and O^T then holds the segment's
+            // tiles before i
+            if (i >= 1) okw = __all_sync(0xffffffffu, wt.wait(pv_done, (i - 1) & 1u));
+            // (a warp's lanes hold every column, with the same values in every warp)
+            raised = __any_sync(0xffffffffu, raised);
+            if (raised && !starts) {
+                if (sw == 0 && lane < 4) {
+#pragma unroll
+                    for (int c = 0; c < NC / 4; ++c) col_s[8 * (c / 2) + cc + c % 2].x = alpha[c];
+                }
+                okw = named_bar_and(1, 4 * 32, okw);
+                if (okw) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int j = 0; j < C::BLOCKS * NC / OW; ++j) {
+                        uint32_t o[OW];
+                        latent_ld_o<OW>(lane_base + C::O_COL + j * OW, o);
+#pragma unroll
+                        for (int c = 0; c < OW; ++c)
+                            o[c] = __float_as_uint(__uint_as_float(o[c]) * col_s[(j * OW) % NC + c].x);
+                        if constexpr (OW == 16)
+                            tmem_st16(lane_base + C::O_COL + j * OW, o);
+                        else
+                            tmem_st32(lane_base + C::O_COL + j * OW, o);
+                    }
+                    tmem_wait_st();
+                }
+            }
+            // Positions no token sees may hold anything (see attn_paged_kernel):
+            // their values are zeroed, each warp's 16 rows by itself. (S(i), which
+            // reads them too, is done.)
+            if (okw && seen_rows != 0xffffu) {
+                okw = __all_sync(0xffffffffu, wt.wait(full(st), (i / NST) & 1u));
+                if (okw && !seen) {
+                    const uint32_t row = ring(st) + my_row * 128;
+                    for (int bx = lane / 16; bx < R / 64; bx += 2)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) st_shared_v4(row + bx * C::BOX_BYTES_T + e * 16, 0u, 0u, 0u, 0u);
+                }
+            }
+            if (okw) {
+                // P^T, rounded to bf16 for the product: row = column of S^T, 64
+                // positions of 2 bytes; the warp's 16 are chunks 2 sw and 2 sw + 1
+                // of its 16-byte chunks
+                const uint32_t j = lane % 8, chunk = 2 * sw + ((lane / 8) & 1);
+                const uint32_t dst = sP + (8 * (lane / 16) + j) * 128 + ((chunk ^ j) * 16);
+#pragma unroll
+                for (int k = 0; k < NK; k += 2) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const __nv_bfloat162 x = __floats2bfloat162_rn(s[4 * k + 2 * v], s[4 * k + 2 * v + 1]);
+                        h[v] = *reinterpret_cast<const uint32_t *>(&x);
+                    }
+                    stmatrix_x4_trans(dst + k * 8 * 128, h[0], h[1], h[2], h[3]);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(p_full);
+            }
+            ok = okw;
+            if (ends) {
+                // ---------------------------------------------------- the segment's results
+                // (the sums go where the maxima of tile i - 1 were)
+                float *const sums = red + (sb ^ 1) * 4 * NC;
+#pragma unroll
+                for (int k = 0; k < NK; ++k) {
+                    float a = l_part[2 * k], b = l_part[2 * k + 1];
+#pragma unroll
+                    for (int o = 4; o <= 16; o *= 2) {
+                        a += __shfl_xor_sync(0xffffffffu, a, o);
+                        b += __shfl_xor_sync(0xffffffffu, b, o);
+                    }
+                    if (lane < 4) {
+                        *reinterpret_cast<float2 *>(sums + sw * NC + 8 * k + cc) = make_float2(a, b);
+                        if (sw == 0) {
+                            col_s[8 * k + cc].y = m_run[2 * k];
+                            col_s[8 * k + cc + 1].y = m_run[2 * k + 1];
+                        }
+                    }
+                }
+                if (ok) ok = __all_sync(0xffffffffu, wt.wait(pv_done, i & 1u));
+                ok = named_bar_and(1, 4 * 32, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const bool whole = seg_j == 0 && cur.last();
+                const int64_t row = static_cast<int64_t>(cur.b) * p.GT + c0;
+                const int64_t slot = paged_slot(blockIdx.x, blockIdx.y, p.split.ranges, cur.b == run.b) * NC;
+                auto sum_of = [&](int c) {
+                    return (sums[c] + sums[NC + c]) + (sums[2 * NC + c] + sums[3 * NC + c]);
+                };
+                for (int c = rank_lane; c < ncol; c += 128) {
+                    const float l = sum_of(c), m = col_s[c].y;
+                    if (whole)
+                        p.lse[row + c] = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
+                    else
+                        p.part_ml[slot + c] = make_float2(m, l);
+                }
+#pragma unroll 1
+                for (int j = 0; j < C::BLOCKS * NC / OW; ++j) {
+                    const int at = (j * OW) / NC * 128 + rank_lane, cj = (j * OW) % NC;
+                    uint32_t o[OW];
+                    latent_ld_o<OW>(lane_base + C::O_COL + j * OW, o);
+#pragma unroll
+                    for (int c = 0; c < OW; ++c) {
+                        if (cj + c < ncol) {
+                            const float v = __uint_as_float(o[c]);
+                            if (whole) {
+                                const float l = sum_of(cj + c);
+                                p.o[(row + cj + c) * R + at] = __float2bfloat16_rn(l == 0.f ? 0.f : v / l);
+                            } else {
+                                p.part_o[(slot + cj + c) * R + at] = v;
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+                // the sums and maxima have been read before the next tile's
+                // maxima, or the next rescaling, overwrite them
+                ok = named_bar_and(1, 4 * 32, ok);
+                if (!ok) break;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+}  // namespace attn_sm100

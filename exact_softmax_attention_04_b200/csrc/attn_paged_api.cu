@@ -10,8 +10,8 @@
 
 #include "attn.h"
 #include "attn_host.h"
+#include "attn_latent_kernel.cuh"
 #include "attn_paged_kernel.cuh"
-#include "attn_paged_simple.cuh"
 
 namespace {
 
@@ -189,8 +189,8 @@ int launch_paged(PagedCall &a)
     CUtensorMap mq, mk, mv;
     const int rows = p.split.B * p.H * p.split.T, box = a.page_size < 128 ? a.page_size : 128;
     if (!encode_rows(enc, &mq, a.q, rows, D, C::N) ||
-        !encode_pool(enc, &mk, a.k, p.num_pages, p.Hkv, a.page_size, D, a.s, box) ||
-        !encode_pool(enc, &mv, a.v, p.num_pages, p.Hkv, a.page_size, D, a.s, box))
+        !encode_pool(enc, &mk, a.k, p.pages.num_pages, p.Hkv, a.page_size, D, a.s, box) ||
+        !encode_pool(enc, &mv, a.v, p.pages.num_pages, p.Hkv, a.page_size, D, a.s, box))
         return ATTN_ERR_CUDA;
     {
         std::lock_guard<std::mutex> lk(g_mu);
@@ -224,10 +224,85 @@ int launch_paged_nc(PagedCall &a, int nc)
     return launch_paged<D, 32>(a);
 }
 
-int launch_simple(attn_sm100::PagedSimpleParams &p, int rows, cudaStream_t st)
+// ---------------------------------------------------------- latent vectors
+
+// Columns a block handles: the query rows H * T, rounded up.
+int latent_columns(int gt) { return gt <= 16 ? 16 : gt <= 32 ? 32 : 64; }
+
+Layout latent_layout(int B, int gt, int max_pages, int page_size, int rank)
 {
-    attn_sm100::attn_paged_simple_kernel<<<static_cast<unsigned>(rows), attn_sm100::SIMPLE_THREADS, 0, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    const int nc = latent_columns(gt);
+    const int64_t cap = static_cast<int64_t>(max_pages) * page_size;
+    const int64_t tiles = B * ((cap + attn_sm100::LATENT_TK - 1) / attn_sm100::LATENT_TK);
+    return make_layout(B, (gt + nc - 1) / nc, tiles, kSMs, nc, rank);
+}
+
+struct LatentCall {
+    const void *q, *pages;
+    int64_t page_stride, token_stride;
+    attn_sm100::LatentParams p;
+    Layout l;
+    uint8_t *workspace;
+    int H, dev, page_size;
+    cudaStream_t st;
+};
+
+// A pool as [page][64-column group][token][column]: boxes of a whole tile where
+// a page holds one, else of a page's tokens and 64 columns.
+bool encode_latent(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, const LatentCall &a, int boxes)
+{
+    const bool whole = a.page_size >= attn_sm100::LATENT_TK;
+    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(a.page_size), static_cast<cuuint64_t>(boxes),
+                                static_cast<cuuint64_t>(a.p.pages.num_pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(a.token_stride) * 2, 128,
+                                   static_cast<cuuint64_t>(a.page_stride) * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(whole ? attn_sm100::LATENT_TK : a.page_size),
+                               static_cast<cuuint32_t>(whole ? boxes : 1), 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(a.pages), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int R, int NC>
+int launch_latent(LatentCall &a)
+{
+    using C = attn_sm100::LatentCfg<R, NC>;
+    static bool set[kMaxDevices] = {};
+    auto enc = encoder();
+    if (!enc) return ATTN_ERR_CUDA;
+    attn_sm100::LatentParams &p = a.p;
+    CUtensorMap mq, mc;
+    const int rows = p.split.B * p.GT;
+    if (!encode_rows(enc, &mq, a.q, rows, R + 64, NC) || !encode_latent(enc, &mc, a, C::BOXES)) return ATTN_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!set[a.dev]) {
+            if (cudaFuncSetAttribute(attn_sm100::attn_latent_kernel<R, NC>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
+                return ATTN_ERR_CUDA;
+            set[a.dev] = true;
+        }
+    }
+    p.split.ranges = a.l.ranges;
+    p.split.before = reinterpret_cast<int *>(a.workspace + a.l.before);
+    p.part_ml = reinterpret_cast<float2 *>(a.workspace + a.l.ml);
+    p.part_o = reinterpret_cast<float *>(a.workspace + a.l.o);
+    const dim3 grid(static_cast<unsigned>(a.l.ranges), static_cast<unsigned>(a.l.units));
+    attn_sm100::attn_latent_kernel<R, NC><<<grid, attn_sm100::LATENT_THREADS, C::SMEM_BYTES, a.st>>>(mq, mc, p);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+    // a sequence of one tile is never split
+    if (p.split.cap <= attn_sm100::LATENT_TK) return ATTN_OK;
+    const attn_sm100::PagedCombine c = {p.split, p.part_o, p.part_ml, p.o, p.lse, a.H, 1, a.l.units};
+    return launch_combine<attn_sm100::LATENT_TK, R, 128, NC>(c, rows, a.st);
+}
+
+template <int R>
+int launch_latent_nc(LatentCall &a, int nc)
+{
+    if (nc == 16) return launch_latent<R, 16>(a);
+    if (nc == 32) return launch_latent<R, 32>(a);
+    return launch_latent<R, 64>(a);
 }
 
 }  // namespace
@@ -268,14 +343,11 @@ extern "C" int attn_decode_paged(const void *q, const void *k_pages, const void 
     a.st = static_cast<cudaStream_t>(stream);
     // (a window past every position is none; kept small, it cannot overflow)
     p.split = {lens, B, T, max_pages * page_size, window < 0 || window >= (1 << 30) ? -1 : window, 0, nullptr};
-    p.table = page_table;
+    p.pages = {page_table, num_pages, max_pages, log2_of(page_size)};
     p.o = static_cast<__nv_bfloat16 *>(o);
     p.lse = lse;
     p.H = H;
     p.Hkv = Hkv;
-    p.num_pages = num_pages;
-    p.max_pages = max_pages;
-    p.page_log2 = log2_of(page_size);
     p.scale_log2 = scale * 1.4426950408889634f;
     const int nc = paged_columns(H / Hkv * T);
     return d == 64 ? launch_paged_nc<64>(a, nc) : launch_paged_nc<128>(a, nc);
@@ -284,7 +356,7 @@ extern "C" int attn_decode_paged(const void *q, const void *k_pages, const void 
 extern "C" int64_t attn_decode_latent_workspace_bytes(int B, int H, int T, int max_pages, int page_size, int rank)
 {
     if (check_latent(B, H, T, 1, page_size, max_pages, rank, 1.f) != ATTN_OK) return -1;
-    return 16;
+    return latent_layout(B, H * T, max_pages, page_size, rank).bytes;
 }
 
 extern "C" int attn_decode_latent(const void *q, const void *pages, const int64_t *strides, const int *page_table,
@@ -301,10 +373,27 @@ extern "C" int attn_decode_latent(const void *q, const void *pages, const int64_
     const int64_t given[3] = {strides ? strides[0] : 0, strides ? strides[0] : 0, strides ? strides[1] : 0};
     int64_t s[3];
     if (take_strides(strides ? given : nullptr, 1, page_size, rank + 64, s) != ATTN_OK) return ATTN_ERR_INVALID;
-    if (workspace_bytes < 16) return ATTN_ERR_INVALID;
-    attn_sm100::PagedSimpleParams p = {
-        static_cast<const __nv_bfloat16 *>(q), static_cast<const __nv_bfloat16 *>(pages),
-        static_cast<const __nv_bfloat16 *>(pages), s[0], s[1], s[2], page_table, lens,
-        static_cast<__nv_bfloat16 *>(o), lse, H, 1, T, num_pages, page_size, max_pages, -1, rank + 64, rank, scale};
-    return launch_simple(p, B * H * T, static_cast<cudaStream_t>(stream));
+    LatentCall a;
+    a.l = latent_layout(B, H * T, max_pages, page_size, rank);
+    if (workspace_bytes < static_cast<size_t>(a.l.bytes)) return ATTN_ERR_INVALID;
+    if (current_device(&a.dev) != ATTN_OK) return ATTN_ERR_CUDA;
+    attn_sm100::LatentParams &p = a.p;
+    p.status = status_word(a.dev);
+    if (!p.status) return ATTN_ERR_CUDA;
+    a.q = q;
+    a.pages = pages;
+    a.page_stride = s[0];
+    a.token_stride = s[2];
+    a.workspace = static_cast<uint8_t *>(workspace);
+    a.H = H;
+    a.page_size = page_size;
+    a.st = static_cast<cudaStream_t>(stream);
+    p.split = {lens, B, T, max_pages * page_size, -1, 0, nullptr};
+    p.pages = {page_table, num_pages, max_pages, log2_of(page_size)};
+    p.o = static_cast<__nv_bfloat16 *>(o);
+    p.lse = lse;
+    p.GT = H * T;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    const int nc = latent_columns(H * T);
+    return rank == 256 ? launch_latent_nc<256>(a, nc) : launch_latent_nc<512>(a, nc);
 }

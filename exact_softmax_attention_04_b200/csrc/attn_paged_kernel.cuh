@@ -30,15 +30,13 @@ namespace attn_sm100 {
 
 struct PagedParams {
     PagedSplit split;
-    const int *table;         // [B, max_pages]
     __nv_bfloat16 *o;         // [B, H, T, D]
     float *lse;               // [B, H, T]
     float *part_o;            // see paged_slot
     float2 *part_ml;
     int *status;
     int H, Hkv, nblk;         // heads; column blocks of a group (gridDim.y = Hkv * nblk)
-    int num_pages, max_pages;
-    int page_log2;
+    PagedTable pages;
     float scale_log2;         // scale * log2(e)
 };
 
@@ -67,13 +65,14 @@ struct PagedCfg {
     // full[NST], empty[NST], q_full[2], q_empty[2], s_full[2], s_free[2], p_full, pv_done, mma_drain
     static constexpr int NBAR = 2 * NST + 11;
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;        // TMEM base, abort flag
-    static constexpr int SMEM_BYTES = MISC_OFF + 16 + 1024;    // + slack to align the base to 1 KB
+    static constexpr int PLAN_OFF = (MISC_OFF + 8 + 15) / 16 * 16;
+    static constexpr int SMEM_BYTES = PLAN_OFF + PLAN_SCRATCH + 1024;  // + slack to align the base to 1 KB
     static constexpr uint32_t TMEM_COLS = N == 16 ? 64 : 128;
     static constexpr uint32_t S_COL = 0;                       // + N * buffer
     static constexpr uint32_t O_COL = 2 * N;
     static_assert(Q_OFF % 1024 == 0 && P_OFF % 1024 == 0 && Q_BYTES % 1024 == 0 && P_BYTES % 1024 == 0,
                   "operand alignment");
-    static_assert(CTAS * (SMEM_BYTES + 1024 + 256) <= 233472, "blocks per SM");
+    static_assert(CTAS * (SMEM_BYTES + 1024) <= 233472, "blocks per SM");
 };
 
 template <int NC>
@@ -98,17 +97,6 @@ __device__ __forceinline__ void paged_tmem_st(uint32_t taddr, const uint32_t (&r
     } else {
         tmem_st32(taddr, r);
     }
-}
-
-// The page that holds positions [at, at + 2^page_log2) of sequence b, at a
-// multiple of the page size; -1 if no token sees one of them or the entry is
-// no page.
-__device__ __forceinline__ int paged_page(const PagedParams &p, const PagedSeq &s, int b, int at)
-{
-    const int lo = p.split.window >= 0 ? max(0, s.len - p.split.T - p.split.window) : 0;
-    if (at >= s.len || at + (1 << p.page_log2) <= lo) return -1;
-    const int page = __ldg(p.table + static_cast<int64_t>(b) * p.max_pages + (at >> p.page_log2));
-    return static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages) ? page : -1;
 }
 
 template <int D, int NC>
@@ -184,7 +172,8 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
         fence_proxy_async_smem();
     }
     tc_fence_before();
-    const PagedRun run = paged_run<PAGED_TK, PAGED_THREADS>(p.split, blockIdx.x);  // synchronises the block
+    // (synchronises the block)
+    const PagedRun run = paged_run<PAGED_TK, PAGED_THREADS>(p.split, blockIdx.x, base_ptr + C::PLAN_OFF);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const Waiter wt{abort_flag, p.status};
@@ -195,14 +184,14 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
     } else if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
         const uint32_t leader = elect_one();
-        const int page = 1 << p.page_log2;
-        const int npg = max(1, PAGED_TK >> p.page_log2);  // pages per tile, one per lane
+        const int page = 1 << p.pages.page_log2;
+        const int npg = max(1, PAGED_TK >> p.pages.page_log2);  // pages per tile, one per lane
         const int rows = min(page, PAGED_TK);
         Walk w;
         w.start(p.split, run.b, run.j);
         auto lane_page = [&]() {
             const int at = w.base() + lane * page;
-            return lane < npg ? paged_page(p, w.s, w.b, npg == 1 ? at & ~(page - 1) : at) : -1;
+            return lane < npg ? paged_page(p.split, p.pages, w.s, w.b, npg == 1 ? at & ~(page - 1) : at) : -1;
         };
         int id = lane_page();
         int items = 0, segs = 0;
@@ -328,7 +317,7 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
         const int window = p.split.window;
         Walk w;
         w.start(p.split, run.b, run.j);
-        auto slot_page = [&]() { return paged_page(p, w.s, w.b, (w.base() + r) & ~((1 << p.page_log2) - 1)); };
+        auto slot_page = [&]() { return paged_page(p.split, p.pages, w.s, w.b, (w.base() + r) & ~((1 << p.pages.page_log2) - 1)); };
         int id = slot_page();
         float m_run[NC], l_part[NC];
         bool ok = true;

@@ -72,16 +72,37 @@ struct PagedWalk {
     __device__ __forceinline__ bool last() const { return j + 1 == s.ntiles; }
 };
 
+struct PagedTable {
+    const int *table;  // [B, max_pages]
+    int num_pages, max_pages;
+    int page_log2;
+};
+
+// The page that holds positions [at, at + 2^page_log2) of sequence b, `at` a
+// multiple of the page size; -1 if no token sees one of them or the entry is
+// no page.
+__device__ __forceinline__ int paged_page(const PagedSplit &p, const PagedTable &t, const PagedSeq &s, int b, int at)
+{
+    const int lo = p.window >= 0 ? max(0, s.len - p.T - p.window) : 0;
+    if (at >= s.len || at + (1 << t.page_log2) <= lo) return -1;
+    const int page = __ldg(t.table + static_cast<int64_t>(b) * t.max_pages + (at >> t.page_log2));
+    return static_cast<unsigned>(page) < static_cast<unsigned>(t.num_pages) ? page : -1;
+}
+
 struct PagedRun {
     int b, j, count;  // first tile, number of tiles (0: none)
 };
 
-// The block's run, for all its NT threads.
+// The block's run, for all its NT threads; `scratch`: PLAN_SCRATCH bytes of
+// shared memory, 16-byte aligned.
+constexpr int PLAN_SCRATCH = 64;
+
 template <int TK, int NT>
-__device__ __forceinline__ PagedRun paged_run(const PagedSplit &p, int r)
+__device__ __forceinline__ PagedRun paged_run(const PagedSplit &p, int r, void *scratch)
 {
-    __shared__ int sums[NT / 32];
-    __shared__ PagedRun run;
+    static_assert(NT / 32 * 4 + 16 <= PLAN_SCRATCH, "scratch");
+    PagedRun &run = *static_cast<PagedRun *>(scratch);
+    int *const sums = static_cast<int *>(scratch) + 4;
     const int tid = threadIdx.x, lane = tid % 32;
     const int per = (p.B + NT - 1) / NT;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
