@@ -18,8 +18,9 @@
 // Roles as in attn_paged_kernel.cuh. With M = 64, S^T lies in the lower 16 lanes
 // of each quarter of TMEM; read as 8 x 8 blocks, all 32 threads of a warp get a
 // share of them, and P^T goes to shared memory by transposing stores. A thread
-// has 2 positions of NC / 4 columns; maxima over a tile go through three
-// shuffles and then between the four warps.
+// has 2 positions of a quarter of the columns; maxima over a tile go through three
+// shuffles and then between the four warps. From 32 columns on, two groups of
+// four warps share the columns out and need nothing of one another.
 #pragma once
 #include "attn_paged_plan.cuh"
 
@@ -38,13 +39,15 @@ struct LatentParams {
 };
 
 constexpr int LATENT_TK = 64;  // positions per tile
-constexpr int LATENT_THREADS = 192;
 constexpr float LATENT_SLACK = 8.f;  // as PAGED_SLACK
 
 template <int R, int NC>
 struct LatentCfg {
     static_assert(R == 256 || R == 512, "rank 256 or 512");
     static_assert(NC == 16 || NC == 32 || NC == 64, "columns");
+    static constexpr int GROUPS = NC == 16 ? 1 : 2;            // softmax warpgroups, which share out the columns
+    static constexpr int CG = NC / GROUPS;                     // columns of each
+    static constexpr int THREADS = 64 + 128 * GROUPS;
     static constexpr int BOXES = R / 64 + 1;                   // 64-column boxes per row
     static constexpr int BLOCKS = R / 128;                     // blocks of O^T
     static constexpr int BOX_BYTES_T = LATENT_TK * 128;        // [64 positions x 64 columns] bf16
@@ -73,17 +76,14 @@ struct LatentCfg {
     static_assert(Q_OFF % 1024 == 0 && P_OFF % 1024 == 0, "operand alignment");
 };
 
-// Warp-uniform read of NC / 2 registers (see tmem_ld_half8).
-template <int NC>
-__device__ __forceinline__ void latent_ld_s(uint32_t taddr, uint32_t (&r)[NC / 2])
+// Reads CG columns of S^T (see tmem_ld_half8).
+template <int CG>
+__device__ __forceinline__ void latent_ld_s(uint32_t taddr, uint32_t (&r)[CG / 2])
 {
-    if constexpr (NC == 16) {
+    if constexpr (CG == 16)
         tmem_ld_half8(taddr, r);
-    } else if constexpr (NC == 32) {
+    else
         tmem_ld_half16(taddr, r);
-    } else {
-        tmem_ld_half32(taddr, r);
-    }
 }
 
 template <int W>
@@ -97,20 +97,19 @@ __device__ __forceinline__ void latent_ld_o(uint32_t taddr, uint32_t (&r)[W])
 }
 
 template <int R, int NC>
-__global__ void __launch_bounds__(LATENT_THREADS, 1)
+__global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
     attn_latent_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
                        const LatentParams p)
 {
     using C = LatentCfg<R, NC>;
     using Walk = PagedWalk<LATENT_TK>;
     constexpr int NST = C::NST;
-    constexpr int NK = NC / 8;  // blocks of 8 columns
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = smem_addr(smem_raw);
     auto ring = [&](int st) { return base + st * C::TILE_BYTES; };
     const uint32_t sQ = base + C::Q_OFF, sP = base + C::P_OFF;
-    float *const red = reinterpret_cast<float *>(smem_raw + C::RED_OFF);
-    float2 *const col_s = reinterpret_cast<float2 *>(smem_raw + C::COL_OFF);
+    float *const red_all = reinterpret_cast<float *>(smem_raw + C::RED_OFF);
+    float2 *const col_all = reinterpret_cast<float2 *>(smem_raw + C::COL_OFF);
     const uint32_t bars = base + C::BAR_OFF;
     auto full = [&](int st) { return bars + 8u * st; };
     auto empty = [&](int st) { return bars + 8u * (NST + st); };
@@ -125,7 +124,6 @@ __global__ void __launch_bounds__(LATENT_THREADS, 1)
     const int lane = static_cast<int>(threadIdx.x % 32);
     const int T = p.split.T;
     const int c0 = blockIdx.y * NC;                  // first column of this block
-    const int ncol = min(p.GT - c0, NC);             // columns in use
 
     grid_dependents_launch();
     if (base % 1024 != 0) {
@@ -142,11 +140,11 @@ __global__ void __launch_bounds__(LATENT_THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full(i), 1);
-            mbar_init(s_free(i), 4 * 32);
+            mbar_init(s_free(i), C::GROUPS * 128);
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
-        mbar_init(p_full, 4 * 32);
+        mbar_init(p_full, C::GROUPS * 128);
         mbar_init(pv_done, 1);
         mbar_init(mma_drain, 1);
         *abort_flag = 0;
@@ -158,7 +156,7 @@ __global__ void __launch_bounds__(LATENT_THREADS, 1)
     }
     tc_fence_before();
     // (synchronises the block)
-    const PagedRun run = paged_run<LATENT_TK, LATENT_THREADS>(p.split, blockIdx.x, smem_raw + C::PLAN_OFF);
+    const PagedRun run = paged_run<LATENT_TK, C::THREADS>(p.split, blockIdx.x, smem_raw + C::PLAN_OFF);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const Waiter wt{abort_flag, p.status};
@@ -312,6 +310,8 @@ __global__ void __launch_bounds__(LATENT_THREADS, 1)
         wt.drain(mma_drain, 0);
     } else {
         // ------------------------------------------------------------ softmax
+        constexpr int CG = C::CG, NK = CG / 8;      // the group's columns, as blocks of 8
+        const int grp = (warp - 2) / 4, g0 = grp * CG;
         const int sw = warp % 4;                    // TMEM quarter: positions 16 sw + 0..15 of the tile
         const int rank_lane = sw * 32 + lane;       // row of an O^T block
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(sw * 32) << 16);
@@ -319,14 +319,15 @@ __global__ void __launch_bounds__(LATENT_THREADS, 1)
         const int rr = lane / 4;                    // its positions: 16 sw + rr and 8 further
         const int my_row = 16 * sw + lane % 16;     // the position whose page this lane looks up
         const float sc = p.scale_log2;
-        constexpr int OW = NC < 32 ? NC : 32;       // columns of O^T read at a time
+        float *const red = red_all + grp * 8 * CG;  // [2][4 warps][CG]
+        float2 *const col_s = col_all + g0;
         Walk w;
         w.start(p.split, run.b, run.j);
         auto row_page = [&]() {
             return paged_page(p.split, p.pages, w.s, w.b, (w.base() + my_row) & ~((1 << p.pages.page_log2) - 1));
         };
         int id = row_page();
-        float m_run[NC / 4], l_part[NC / 4];
+        float m_run[CG / 4], l_part[CG / 4];
         bool ok = true;
         int seg_j = run.j;  // where the segment began
         for (int i = 0; i < count; ++i) {
@@ -345,26 +346,26 @@ __global__ void __launch_bounds__(LATENT_THREADS, 1)
             }
             if (starts) {
 #pragma unroll
-                for (int c = 0; c < NC / 4; ++c) {
+                for (int c = 0; c < CG / 4; ++c) {
                     m_run[c] = -CUDART_INF_F;
                     l_part[c] = 0.f;
                 }
                 seg_j = cur.j;
             }
             bool okw = __all_sync(0xffffffffu, wt.wait(s_full(sb), (i / 2) & 1u));
-            float s[NC / 2];  // [8-column block][position rr, rr + 8][column]
+            float s[CG / 2];  // [8-column block][position rr, rr + 8][column]
             if (okw) {
                 tc_fence_after();
-                uint32_t sv[NC / 2];
-                latent_ld_s<NC>(lane_base + NC * sb, sv);
+                uint32_t sv[CG / 2];
+                latent_ld_s<CG>(lane_base + NC * sb + g0, sv);
                 tc_fence_before();
                 mbar_arrive(s_free(sb));
 #pragma unroll
-                for (int e = 0; e < NC / 2; ++e) s[e] = __uint_as_float(sv[e]) * sc;
+                for (int e = 0; e < CG / 2; ++e) s[e] = __uint_as_float(sv[e]) * sc;
                 if (!plain) {
 #pragma unroll
-                    for (int e = 0; e < NC / 2; ++e) {
-                        const int row = rr + ((e & 2) ? 8 : 0), c = c0 + 8 * (e / 4) + cc + (e & 1);
+                    for (int e = 0; e < CG / 2; ++e) {
+                        const int row = rr + ((e & 2) ? 8 : 0), c = c0 + g0 + 8 * (e / 4) + cc + (e & 1);
                         const int at = cur.base() + 16 * sw + row;
                         const bool allowed = ((seen_rows >> row) & 1u) && at <= len - T + c % T;
                         s[e] = allowed ? s[e] : -CUDART_INF_F;
@@ -379,20 +380,20 @@ __global__ void __launch_bounds__(LATENT_THREADS, 1)
                         b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
                     }
                     if (lane < 4)
-                        *reinterpret_cast<float2 *>(red + (sb * 4 + sw) * NC + 8 * k + cc) = make_float2(a, b);
+                        *reinterpret_cast<float2 *>(red + (sb * 4 + sw) * CG + 8 * k + cc) = make_float2(a, b);
                 }
             }
             // (ok carries a wait that gave up later in the previous tile)
-            ok = named_bar_and(1, 4 * 32, okw && ok);
+            ok = named_bar_and(1 + grp, 4 * 32, okw && ok);
             if (!ok) break;
-            float alpha[NC / 4];
+            float alpha[CG / 4];
             bool raised = false;
 #pragma unroll
             for (int k = 0; k < NK; ++k) {
-                float2 mx = *reinterpret_cast<const float2 *>(red + sb * 4 * NC + 8 * k + cc);
+                float2 mx = *reinterpret_cast<const float2 *>(red + sb * 4 * CG + 8 * k + cc);
 #pragma unroll
                 for (int v = 1; v < 4; ++v) {
-                    const float2 t = *reinterpret_cast<const float2 *>(red + (sb * 4 + v) * NC + 8 * k + cc);
+                    const float2 t = *reinterpret_cast<const float2 *>(red + (sb * 4 + v) * CG + 8 * k + cc);
                     mx.x = fmaxf(mx.x, t.x);
                     mx.y = fmaxf(mx.y, t.y);
                 }
@@ -422,22 +423,22 @@ __global__ void __launch_bounds__(LATENT_THREADS, 1)
             if (raised && !starts) {
                 if (sw == 0 && lane < 4) {
 #pragma unroll
-                    for (int c = 0; c < NC / 4; ++c) col_s[8 * (c / 2) + cc + c % 2].x = alpha[c];
+                    for (int c = 0; c < CG / 4; ++c) col_s[8 * (c / 2) + cc + c % 2].x = alpha[c];
                 }
-                okw = named_bar_and(1, 4 * 32, okw);
+                okw = named_bar_and(1 + grp, 4 * 32, okw);
                 if (okw) {
                     tc_fence_after();
 #pragma unroll 1
-                    for (int j = 0; j < C::BLOCKS * NC / OW; ++j) {
-                        uint32_t o[OW];
-                        latent_ld_o<OW>(lane_base + C::O_COL + j * OW, o);
+                    for (int blk = 0; blk < C::BLOCKS; ++blk) {
+                        const uint32_t at = lane_base + C::O_COL + blk * NC + g0;
+                        uint32_t o[CG];
+                        latent_ld_o<CG>(at, o);
 #pragma unroll
-                        for (int c = 0; c < OW; ++c)
-                            o[c] = __float_as_uint(__uint_as_float(o[c]) * col_s[(j * OW) % NC + c].x);
-                        if constexpr (OW == 16)
-                            tmem_st16(lane_base + C::O_COL + j * OW, o);
+                        for (int c = 0; c < CG; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * col_s[c].x);
+                        if constexpr (CG == 16)
+                            tmem_st16(at, o);
                         else
-                            tmem_st32(lane_base + C::O_COL + j * OW, o);
+                            tmem_st32(at, o);
                     }
                     tmem_wait_st();
                 }
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(LATENT_THREADS, 1)
                 okw = __all_sync(0xffffffffu, wt.wait(full(st), (i / NST) & 1u));
                 if (okw && !seen) {
                     const uint32_t row = ring(st) + my_row * 128;
-                    for (int bx = lane / 16; bx < R / 64; bx += 2)
+                    for (int bx = 2 * grp + lane / 16; bx < R / 64; bx += 2 * C::GROUPS)
 #pragma unroll
                         for (int e = 0; e < 8; ++e) st_shared_v4(row + bx * C::BOX_BYTES_T + e * 16, 0u, 0u, 0u, 0u);
                 }
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(LATENT_THREADS, 1)
                 // positions of 2 bytes; the warp's 16 are chunks 2 sw and 2 sw + 1
                 // of its 16-byte chunks
                 const uint32_t j = lane % 8, chunk = 2 * sw + ((lane / 8) & 1);
-                const uint32_t dst = sP + (8 * (lane / 16) + j) * 128 + ((chunk ^ j) * 16);
+                const uint32_t dst = sP + (g0 + 8 * (lane / 16) + j) * 128 + ((chunk ^ j) * 16);
 #pragma unroll
                 for (int k = 0; k < NK; k += 2) {
                     uint32_t h[4];
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(LATENT_THREADS, 1)
             if (ends) {
                 // ---------------------------------------------------- the segment's results
                 // (the sums go where the maxima of tile i - 1 were)
-                float *const sums = red + (sb ^ 1) * 4 * NC;
+                float *const sums = red + (sb ^ 1) * 4 * CG;
 #pragma unroll
                 for (int k = 0; k < NK; ++k) {
                     float a = l_part[2 * k], b = l_part[2 * k + 1];
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(LATENT_THREADS, 1)
                         b += __shfl_xor_sync(0xffffffffu, b, o);
                     }
                     if (lane < 4) {
-                        *reinterpret_cast<float2 *>(sums + sw * NC + 8 * k + cc) = make_float2(a, b);
+                        *reinterpret_cast<float2 *>(sums + sw * CG + 8 * k + cc) = make_float2(a, b);
                         if (sw == 0) {
                             col_s[8 * k + cc].y = m_run[2 * k];
                             col_s[8 * k + cc + 1].y = m_run[2 * k + 1];
@@ -496,14 +497,15 @@ __global__ void __launch_bounds__(LATENT_THREADS, 1)
                     }
                 }
                 if (ok) ok = __all_sync(0xffffffffu, wt.wait(pv_done, i & 1u));
-                ok = named_bar_and(1, 4 * 32, ok);
+                ok = named_bar_and(1 + grp, 4 * 32, ok);
                 if (!ok) break;
                 tc_fence_after();
+                const int ncol = min(p.GT - c0 - g0, CG);  // the group's columns in use
                 const bool whole = seg_j == 0 && cur.last();
-                const int64_t row = static_cast<int64_t>(cur.b) * p.GT + c0;
-                const int64_t slot = paged_slot(blockIdx.x, blockIdx.y, p.split.ranges, cur.b == run.b) * NC;
+                const int64_t row = static_cast<int64_t>(cur.b) * p.GT + c0 + g0;
+                const int64_t slot = paged_slot(blockIdx.x, blockIdx.y, p.split.ranges, cur.b == run.b) * NC + g0;
                 auto sum_of = [&](int c) {
-                    return (sums[c] + sums[NC + c]) + (sums[2 * NC + c] + sums[3 * NC + c]);
+                    return (sums[c] + sums[CG + c]) + (sums[2 * CG + c] + sums[3 * CG + c]);
                 };
                 for (int c = rank_lane; c < ncol; c += 128) {
                     const float l = sum_of(c), m = col_s[c].y;
@@ -513,19 +515,19 @@ __global__ void __launch_bounds__(LATENT_THREADS, 1)
                         p.part_ml[slot + c] = make_float2(m, l);
                 }
 #pragma unroll 1
-                for (int j = 0; j < C::BLOCKS * NC / OW; ++j) {
-                    const int at = (j * OW) / NC * 128 + rank_lane, cj = (j * OW) % NC;
-                    uint32_t o[OW];
-                    latent_ld_o<OW>(lane_base + C::O_COL + j * OW, o);
+                for (int blk = 0; blk < C::BLOCKS; ++blk) {
+                    const int at = blk * 128 + rank_lane;
+                    uint32_t o[CG];
+                    latent_ld_o<CG>(lane_base + C::O_COL + blk * NC + g0, o);
 #pragma unroll
-                    for (int c = 0; c < OW; ++c) {
-                        if (cj + c < ncol) {
+                    for (int c = 0; c < CG; ++c) {
+                        if (c < ncol) {
                             const float v = __uint_as_float(o[c]);
                             if (whole) {
-                                const float l = sum_of(cj + c);
-                                p.o[(row + cj + c) * R + at] = __float2bfloat16_rn(l == 0.f ? 0.f : v / l);
+                                const float l = sum_of(c);
+                                p.o[(row + c) * R + at] = __float2bfloat16_rn(l == 0.f ? 0.f : v / l);
                             } else {
-                                p.part_o[(slot + cj + c) * R + at] = v;
+                                p.part_o[(slot + c) * R + at] = v;
                             }
                         }
                     }
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(LATENT_THREADS, 1)
                 tc_fence_before();
                 // the sums and maxima have been read before the next tile's
                 // maxima, or the next rescaling, overwrite them
-                ok = named_bar_and(1, 4 * 32, ok);
+                ok = named_bar_and(1 + grp, 4 * 32, ok);
                 if (!ok) break;
             }
         }

@@ -102,11 +102,18 @@ Layout make_layout(int B, int units, int64_t max_tiles, int resident, int nc, in
 
 // The joining kernel, which starts while the one before still runs and waits
 // for it.
-template <int TK, int DV, int DC, int NC>
-int launch_combine(const attn_sm100::PagedCombine &a, int rows, cudaStream_t st)
+template <int TK, int DV, int NC>
+int launch_combine(attn_sm100::PagedCombine a, cudaStream_t st)
 {
+    // a block of 256 threads for each column while there are few, up to 16
+    // columns a block where that still leaves two blocks an SM
+    const int gt = a.H / a.Hkv * a.split.T, cols = gt < NC ? gt : NC;
+    const int64_t rows = static_cast<int64_t>(a.split.B) * a.H * a.split.T;
+    a.per_block = 1;
+    while (a.per_block < 16 && a.per_block < cols && rows / (2 * a.per_block) >= 2 * kSMs) a.per_block *= 2;
+    const int64_t blocks = static_cast<int64_t>(a.split.B) * a.Hkv * a.nblk * ((cols + a.per_block - 1) / a.per_block);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(rows), DV / DC);
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(attn_sm100::COMBINE_THREADS);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -114,7 +121,7 @@ int launch_combine(const attn_sm100::PagedCombine &a, int rows, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_sm100::attn_paged_combine_kernel<TK, DV, DC, NC>, a) == cudaSuccess
+    return cudaLaunchKernelEx(&cfg, attn_sm100::attn_paged_combine_kernel<TK, DV, NC>, a) == cudaSuccess
                ? ATTN_OK
                : ATTN_ERR_CUDA;
 }
@@ -211,8 +218,8 @@ int launch_paged(PagedCall &a)
     if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
     // a sequence of one tile is never split
     if (p.split.cap <= attn_sm100::PAGED_TK) return ATTN_OK;
-    const attn_sm100::PagedCombine c = {p.split, p.part_o, p.part_ml, p.o, p.lse, p.H, p.Hkv, p.nblk};
-    return launch_combine<attn_sm100::PAGED_TK, D, D, NC>(c, rows, a.st);
+    const attn_sm100::PagedCombine c = {p.split, p.part_o, p.part_ml, p.o, p.lse, p.H, p.Hkv, p.nblk, 1};
+    return launch_combine<attn_sm100::PAGED_TK, D, NC>(c, a.st);
 }
 
 template <int D>
@@ -289,12 +296,12 @@ int launch_latent(LatentCall &a)
     p.part_ml = reinterpret_cast<float2 *>(a.workspace + a.l.ml);
     p.part_o = reinterpret_cast<float *>(a.workspace + a.l.o);
     const dim3 grid(static_cast<unsigned>(a.l.ranges), static_cast<unsigned>(a.l.units));
-    attn_sm100::attn_latent_kernel<R, NC><<<grid, attn_sm100::LATENT_THREADS, C::SMEM_BYTES, a.st>>>(mq, mc, p);
+    attn_sm100::attn_latent_kernel<R, NC><<<grid, C::THREADS, C::SMEM_BYTES, a.st>>>(mq, mc, p);
     if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
     // a sequence of one tile is never split
     if (p.split.cap <= attn_sm100::LATENT_TK) return ATTN_OK;
-    const attn_sm100::PagedCombine c = {p.split, p.part_o, p.part_ml, p.o, p.lse, a.H, 1, a.l.units};
-    return launch_combine<attn_sm100::LATENT_TK, R, 128, NC>(c, rows, a.st);
+    const attn_sm100::PagedCombine c = {p.split, p.part_o, p.part_ml, p.o, p.lse, a.H, 1, a.l.units, 1};
+    return launch_combine<attn_sm100::LATENT_TK, R, NC>(c, a.st);
 }
 
 template <int R>

@@ -167,29 +167,34 @@ struct PagedCombine {
     __nv_bfloat16 *o;  // [B, H, T, DV]
     float *lse;        // [B, H, T]
     int H, Hkv, nblk;  // heads; column blocks of a group
+    int per_block;     // columns a block joins
 };
 
 constexpr int COMBINE_THREADS = 256;
 
-// Joins the segments of one query row (grid x), DC of its DV columns (grid y):
+// Joins the segments of `per_block` columns of one (sequence, y) pair:
 //   M = max_s m_s, l = sum_s l_s 2^(m_s - M), O = sum_s O_s 2^(m_s - M) / l.
-// DC / 4 lanes take 16 bytes each of a segment, and the groups of lanes take
-// the segments in turn, so that a hundred segments of a long sequence are a
-// dozen loads deep. Which segments there are follows from the lengths alone
-// and is worked out while the kernel before is still running.
-template <int TK, int DV, int DC, int NC>
+// DV / 4 lanes take 16 bytes each of a segment. With few segments the groups of
+// lanes take the columns in turn, with many they take the segments, so that a
+// hundred segments of a long sequence are a dozen loads deep. Which segments
+// there are follows from the lengths alone and is worked out while the kernel
+// before is still running.
+template <int TK, int DV, int NC>
 __global__ void __launch_bounds__(COMBINE_THREADS) attn_paged_combine_kernel(const PagedCombine a)
 {
-    constexpr int LANES = DC / 4, GROUPS = COMBINE_THREADS / LANES;
+    constexpr int LANES = DV / 4, GROUPS = COMBINE_THREADS / LANES;
+    constexpr int FEW = 6;
     __shared__ int red[2][COMBINE_THREADS / 32];
     __shared__ float4 acc_s[GROUPS][LANES];
     __shared__ float l_s[GROUPS];
     const PagedSplit &p = a.split;
-    const int row = blockIdx.x, tid = threadIdx.x;
-    const int G = a.H / a.Hkv, GT = G * p.T;
-    const int unit = row / GT;  // b * Hkv + key/value head
-    const int b = unit / a.Hkv, gc = row % GT;
-    const int y = (unit % a.Hkv) * a.nblk + gc / NC, c = gc % NC;
+    const int tid = threadIdx.x;
+    const int G = a.H / a.Hkv, GT = G * p.T, units = a.Hkv * a.nblk;
+    const int per_unit = (min(GT, NC) + a.per_block - 1) / a.per_block;
+    const int b = blockIdx.x / per_unit / units, y = blockIdx.x / per_unit % units;
+    const int head = y / a.nblk, c0 = y % a.nblk * NC;
+    const int c_begin = blockIdx.x % per_unit * a.per_block;
+    const int c_end = min(c_begin + a.per_block, min(GT - c0, NC));
 
     int before = 0, total = 0;
     if (p.B <= COMBINE_SCAN) {
@@ -227,52 +232,76 @@ __global__ void __launch_bounds__(COMBINE_THREADS) attn_paged_combine_kernel(con
     const int nseg = r1 - r0 + 1;
     // run r0 may begin before the sequence; then this is its last segment
     const bool r0_first = paged_run_start(total, r0, n) >= before;
-    auto slot = [&](int s) { return paged_slot(r0 + s, y, p.ranges, s > 0 || r0_first) * NC + c; };
-
-    grid_dependency_wait();
-    if (r0 == r1) return;  // one block had the whole sequence
-
-    float M = -CUDART_INF_F;
-    for (int s = tid % 32; s < nseg; s += 32) M = fmaxf(M, a.part_ml[slot(s)].x);
-    M = redux_max(M);
-    const float ref = M == -CUDART_INF_F ? 0.f : M;
+    auto slot = [&](int s, int c) { return paged_slot(r0 + s, y, p.ranges, s > 0 || r0_first) * NC + c; };
     const int g = tid / LANES, e = tid % LANES;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int s = g; s < nseg; s += GROUPS) {
-        const int64_t at = slot(s);
+    const int64_t row0 = (static_cast<int64_t>(b) * a.H + head * G) * p.T + c0;
+
+    auto add = [&](float4 &acc, float &l, int64_t at, float ref) {
         const float2 ml = a.part_ml[at];
-        const float4 v = *reinterpret_cast<const float4 *>(a.part_o + at * DV + blockIdx.y * DC + 4 * e);
+        const float4 v = *reinterpret_cast<const float4 *>(a.part_o + at * DV + 4 * e);
         const float f = ex2_approx(ml.x - ref);  // 0 for a segment without a position
         l = fmaf(ml.y, f, l);
         acc.x = fmaf(v.x, f, acc.x);
         acc.y = fmaf(v.y, f, acc.y);
         acc.z = fmaf(v.z, f, acc.z);
         acc.w = fmaf(v.w, f, acc.w);
-    }
-    acc_s[g][e] = acc;
-    if (e == 0) l_s[g] = l;
-    __syncthreads();
-    if (g != 0) return;
+    };
+    auto write = [&](const float4 &acc, float l, float M, int c) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        uint2 w;
+        w.x = *reinterpret_cast<const uint32_t *>(&lo);
+        w.y = *reinterpret_cast<const uint32_t *>(&hi);
+        *reinterpret_cast<uint2 *>(a.o + (row0 + c) * DV + 4 * e) = w;
+        if (e == 0) a.lse[row0 + c] = l == 0.f ? -CUDART_INF_F : (M + __log2f(l)) * 0.69314718055994531f;
+    };
+
+    grid_dependency_wait();
+    if (nseg == 1) return;  // one block had the whole sequence
+
+    if (nseg <= FEW) {
+        for (int c = c_begin + g; c < c_end; c += GROUPS) {
+            float M = -CUDART_INF_F;
 #pragma unroll
-    for (int i = 1; i < GROUPS; ++i) {
-        const float4 v = acc_s[i][e];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
-        l += l_s[i];
+            for (int s = 0; s < FEW; ++s)
+                if (s < nseg) M = fmaxf(M, a.part_ml[slot(s, c)].x);
+            const float ref = M == -CUDART_INF_F ? 0.f : M;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float l = 0.f;
+#pragma unroll
+            for (int s = 0; s < FEW; ++s)
+                if (s < nseg) add(acc, l, slot(s, c), ref);
+            write(acc, l, M, c);
+        }
+        return;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-    uint2 w;
-    w.x = *reinterpret_cast<const uint32_t *>(&lo);
-    w.y = *reinterpret_cast<const uint32_t *>(&hi);
-    *reinterpret_cast<uint2 *>(a.o + static_cast<int64_t>(row) * DV + blockIdx.y * DC + 4 * e) = w;
-    if (e == 0 && blockIdx.y == 0)
-        a.lse[row] = l == 0.f ? -CUDART_INF_F : (M + __log2f(l)) * 0.69314718055994531f;
+    for (int c = c_begin; c < c_end; ++c) {
+        float M = -CUDART_INF_F;
+        for (int s = tid % 32; s < nseg; s += 32) M = fmaxf(M, a.part_ml[slot(s, c)].x);
+        M = redux_max(M);
+        const float ref = M == -CUDART_INF_F ? 0.f : M;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+#pragma unroll 8
+        for (int s = g; s < nseg; s += GROUPS) add(acc, l, slot(s, c), ref);
+        acc_s[g][e] = acc;
+        if (e == 0) l_s[g] = l;
+        __syncthreads();
+        if (g == 0) {
+#pragma unroll
+            for (int i = 1; i < GROUPS; ++i) {
+                const float4 v = acc_s[i][e];
+                acc.x += v.x;
+                acc.y += v.y;
+                acc.z += v.z;
+                acc.w += v.w;
+                l += l_s[i];
+            }
+            write(acc, l, M, c);
+        }
+        __syncthreads();
+    }
 }
 
 }  // namespace attn_sm100

@@ -365,18 +365,6 @@ __device__ __forceinline__ void tmem_ld_half16(uint32_t taddr, uint32_t (&r)[16]
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld_half32(uint32_t taddr, uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : ATTN_R8(0), ATTN_R8(8), ATTN_R8(16), ATTN_R8(24)
-        : "r"(taddr)
-        : "memory");
-}
-
 // Four 8 x 8 blocks of 16-bit values, held as above (two columns a register),
 // to shared memory transposed: lane l gives the address of 16 bytes for column
 // l % 8 of block l / 8.
