@@ -387,18 +387,27 @@ def attn_decode_multi(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
 # ---------------------------------------------------------------------------
 # Paged caches (see "Paged caches" in include/attn.h)
 
-def _check_ints(device: torch.device, **tensors) -> None:
-    """Each of ``tensors`` (name=(tensor, shape)) an int32 tensor on ``device``."""
-    for name, (t, shape) in tensors.items():
-        if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or t.shape != shape:
-            raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on the pages' device")
+# These calls are made every step and often on little data, so what a call
+# costs on the host counts: tensors are looked at once each, and the current
+# device and stream are switched only if they are not the right ones already.
+
+def _elsewhere(stream: Optional[torch.cuda.Stream], device: torch.device):
+    """None if a call on ``device`` can go to the current stream; else a context
+    in which it can: there, what the call allocates belongs to its stream."""
+    if stream is None:
+        return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError("stream must be on the tensors' device")
+    return torch.cuda.stream(stream)
 
 
-def _check_pool(name: str, pool: torch.Tensor) -> None:
-    if pool.dtype != torch.bfloat16 or not pool.is_cuda:
-        raise ValueError(f"{name} must be a bf16 CUDA tensor")
-    if pool.stride(-1) != 1 and pool.shape[-1] != 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
+def _raw_stream(device: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _check_int(name: str, t: torch.Tensor, device: torch.device, *shape: int) -> None:
+    if t.dtype is not torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on the pages' device")
 
 
 def _strides(t: torch.Tensor, at_least: int):
@@ -408,7 +417,14 @@ def _strides(t: torch.Tensor, at_least: int):
     if t.is_contiguous():
         return None
     n = t.dim() - 1
-    return (ctypes.c_int64 * n)(*(t.stride(j) if t.shape[j] > 1 else at_least for j in range(n)))
+    return (ctypes.c_int64 * n)(*[x if m > 1 else at_least for x, m in zip(t.stride()[:n], t.shape)])
+
+
+def _check_pool(name: str, pool: torch.Tensor) -> None:
+    if pool.dtype is not torch.bfloat16 or not pool.is_cuda:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor")
+    if pool.stride(-1) != 1 and pool.shape[-1] != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
 
 
 def _pools(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor]):
@@ -419,43 +435,59 @@ def _pools(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor]):
             k_pages = k_pages.unsqueeze(1)
         if k_pages.dim() != 4:
             raise ValueError("a single pool must be [num_pages, page_size, d] or [num_pages, Hkv, page_size, d]")
-    else:
-        _check_pool("v_pages", v_pages)
-        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.device != v_pages.device:
-            raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, d], alike and on one device")
-    P, Hkv, page, d = k_pages.shape
-    strides = _strides(k_pages, d)
-    if v_pages is not None:
-        other = _strides(v_pages, d)
-        if (strides is None) != (other is None) or (strides is not None and list(strides) != list(other)):
-            raise ValueError("k_pages and v_pages must have the same strides")
+        P, Hkv, page, d = k_pages.shape
+        return Hkv, P, page, d, _strides(k_pages, d)
+    _check_pool("v_pages", v_pages)
+    shape = k_pages.shape
+    if len(shape) != 4 or shape != v_pages.shape or k_pages.device != v_pages.device:
+        raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, d], alike and on one device")
+    P, Hkv, page, d = shape
+    strides, other = _strides(k_pages, d), _strides(v_pages, d)
+    if (strides is None) != (other is None) or (strides is not None and strides[:] != other[:]):
+        raise ValueError("k_pages and v_pages must have the same strides")
     return Hkv, P, page, d, strides
 
 
 def _outputs(q: torch.Tensor, width: int, out: Optional[torch.Tensor], lse: Optional[torch.Tensor]):
-    shape, rows = q.shape[:-1] + (width,), q.shape[:-1]
+    rows = q.shape[:-1]
+    shape = rows + (width,)
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-    elif out.shape != shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != q.device:
+    elif out.shape != shape or out.dtype is not torch.bfloat16 or not out.is_contiguous() or out.device != q.device:
         raise ValueError(f"out must be a contiguous bf16 tensor {list(shape)} on q's device")
     if lse is None:
         lse = torch.empty(rows, dtype=torch.float32, device=q.device)
-    elif lse.shape != rows or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != q.device:
+    elif lse.shape != rows or lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.device != q.device:
         raise ValueError(f"lse must be a contiguous fp32 tensor {list(rows)} on q's device")
     return out, lse
 
 
-def _scratch(workspace: Optional[torch.Tensor], need: int, device: torch.device) -> torch.Tensor:
+def _scratch(workspace: Optional[torch.Tensor], need, sizes: tuple, device: torch.device) -> Tuple[torch.Tensor, int]:
+    """A workspace and its bytes: the caller's, or one of need(*sizes) bytes."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        n = need(*sizes)
+        return torch.empty(n, dtype=torch.uint8, device=device), n
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the pages' device")
-    return workspace
+    return workspace, workspace.nbytes
+
+
+def _check_queries(q: torch.Tensor, pages: torch.Tensor, d: int, page_table: torch.Tensor,
+                   lens: torch.Tensor) -> Tuple[int, int, int, int]:
+    """(B, H, T, max_pages)."""
+    if q.dtype is not torch.bfloat16 or q.device != pages.device or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 tensor on the pages' device")
+    shape, width = q.shape, page_table.shape[-1]
+    if len(shape) not in (3, 4) or shape[-1] != d:
+        raise ValueError("q must be [B, H, T, x] or [B, H, x] with x the length of the pages' rows")
+    B = shape[0]
+    _check_int("page_table", page_table, q.device, B, width)
+    _check_int("lens", lens, q.device, B)
+    return B, shape[1], shape[2] if len(shape) == 4 else 1, width
 
 
 def decode_paged_workspace_bytes(B: int, H: int, Hkv: int, T: int, max_pages: int, page_size: int, d: int) -> int:
-    r = int(lib().attn_decode_paged_workspace_bytes(int(B), int(H), int(Hkv), int(T), int(max_pages),
-                                                    int(page_size), int(d)))
+    r = lib().attn_decode_paged_workspace_bytes(B, H, Hkv, T, max_pages, page_size, d)
     if r < 0:
         raise ValueError("unsupported or invalid shape for attn_decode_paged")
     return r
@@ -476,35 +508,24 @@ def attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
     q, lse fp32 without the last dimension); a token that sees no position
     gets 0 and -inf. See include/attn.h."""
     Hkv, P, page, d, strides = _pools(k_pages, v_pages)
-    if q.dtype != torch.bfloat16 or q.device != k_pages.device or not q.is_contiguous():
-        raise ValueError("q must be a contiguous bf16 tensor on the pages' device")
-    if q.dim() not in (3, 4) or q.shape[-1] != d:
-        raise ValueError("q must be [B, H, T, d] or [B, H, d] with the pages' d")
-    B, H, T = q.shape[0], q.shape[1], q.shape[2] if q.dim() == 4 else 1
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages]")
-    width = page_table.shape[1]
-    _check_ints(q.device, page_table=(page_table, (B, width)), lens=(lens, (B,)))
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    if workspace is None:
-        workspace = _scratch(None, decode_paged_workspace_bytes(B, H, Hkv, T, width, page, d), q.device)
-    else:
-        _scratch(workspace, 0, q.device)
+    B, H, T, width = _check_queries(q, k_pages, d, page_table, lens)
+    there = _elsewhere(stream, q.device)
+    if there is not None:
+        with there:
+            return attn_decode_paged(q, k_pages, v_pages, page_table, lens, window, scale, out, lse, workspace)
+    workspace, size = _scratch(workspace, decode_paged_workspace_bytes, (B, H, Hkv, T, width, page, d), q.device)
     out, lse = _outputs(q, d, out, lse)
-    with torch.cuda.device(q.device):
-        rc = lib().attn_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), strides,
-                                     page_table.data_ptr(), lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(), B, H, Hkv,
-                                     T, P, page, width, int(window), d, float(scale), _stream_handle(stream))
+    rc = lib().attn_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), strides,
+                                 page_table.data_ptr(), lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                 workspace.data_ptr(), size, B, H, Hkv, T, P, page, width, window, d,
+                                 1.0 / math.sqrt(d) if scale is None else scale, _raw_stream(q.device))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode_paged")
     return out, lse
 
 
 def decode_latent_workspace_bytes(B: int, H: int, T: int, max_pages: int, page_size: int, rank: int) -> int:
-    r = int(lib().attn_decode_latent_workspace_bytes(int(B), int(H), int(T), int(max_pages), int(page_size),
-                                                     int(rank)))
+    r = lib().attn_decode_latent_workspace_bytes(B, H, T, max_pages, page_size, rank)
     if r < 0:
         raise ValueError("unsupported or invalid shape for attn_decode_latent")
     return r
@@ -524,29 +545,21 @@ def attn_decode_latent(q: torch.Tensor, pages: torch.Tensor, page_table: torch.T
     (rank does not tell it). Returns (o [B, H, T, rank] or [B, H, rank], lse
     fp32). See include/attn.h."""
     Hkv, P, page, D, strides = _pools(pages, None)
-    if Hkv != 1:
+    if Hkv != 1 or D <= 64:
         raise ValueError("pages must be [num_pages, page_size, rank + 64]")
-    if q.dtype != torch.bfloat16 or q.device != pages.device or not q.is_contiguous():
-        raise ValueError("q must be a contiguous bf16 tensor on the pages' device")
-    if q.dim() not in (3, 4) or q.shape[-1] != D or D <= 64:
-        raise ValueError("q must be [B, H, T, rank + 64] or [B, H, rank + 64] with the pages' row length")
-    B, H, T = q.shape[0], q.shape[1], q.shape[2] if q.dim() == 4 else 1
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages]")
-    width, rank = page_table.shape[1], D - 64
-    _check_ints(q.device, page_table=(page_table, (B, width)), lens=(lens, (B,)))
-    if workspace is None:
-        workspace = _scratch(None, decode_latent_workspace_bytes(B, H, T, width, page, rank), q.device)
-    else:
-        _scratch(workspace, 0, q.device)
+    B, H, T, width = _check_queries(q, pages, D, page_table, lens)
+    there = _elsewhere(stream, q.device)
+    if there is not None:
+        with there:
+            return attn_decode_latent(q, pages, page_table, lens, scale, out, lse, workspace)
+    rank = D - 64
+    workspace, size = _scratch(workspace, decode_latent_workspace_bytes, (B, H, T, width, page, rank), q.device)
     out, lse = _outputs(q, rank, out, lse)
     if strides is not None:
         strides = (ctypes.c_int64 * 2)(strides[0], strides[2])
-    with torch.cuda.device(q.device):
-        rc = lib().attn_decode_latent(q.data_ptr(), pages.data_ptr(), strides, page_table.data_ptr(),
-                                      lens.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-                                      workspace.numel() * workspace.element_size(), B, H, T, P, page, width, rank,
-                                      float(scale), _stream_handle(stream))
+    rc = lib().attn_decode_latent(q.data_ptr(), pages.data_ptr(), strides, page_table.data_ptr(), lens.data_ptr(),
+                                  out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size, B, H, T, P, page,
+                                  width, rank, scale, _raw_stream(q.device))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode_latent")
     return out, lse
@@ -560,51 +573,53 @@ def pages_append(k: torch.Tensor, v: Optional[torch.Tensor], k_pages: torch.Tens
     k, v: bf16 [B, Hkv, T, d] of any strides whose last is 1; token u < count[b]
     (default T) goes to position pos[b] + u. A single pool, [num_pages,
     page_size, d] (latent rows: k [B, 1, T, d]) or with heads as above, has
-    v = v_pages = None.
-    page_table int32 [B, max_pages], pos and count int32 [B]."""
+    v = v_pages = None. page_table int32 [B, max_pages], pos and count int32
+    [B]."""
     if (v is None) != (v_pages is None):
         raise ValueError("v and v_pages go together")
     Hkv, P, page, d, strides = _pools(k_pages, v_pages)
-    news = [(k, "k")] + ([(v, "v")] if v is not None else [])
-    for t, name in news:
-        if t.dtype != torch.bfloat16 or t.device != k_pages.device or t.dim() != 4 or t.shape != k.shape or \
-                t.shape[1] != Hkv or t.shape[3] != d or t.stride(3) != 1:
-            raise ValueError(f"{name} must be a bf16 tensor [B, Hkv, T, d] on the pages' device, last stride 1")
-    B, _, T, _ = k.shape
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages]")
-    width = page_table.shape[1]
-    _check_ints(k.device, page_table=(page_table, (B, width)), pos=(pos, (B,)))
+    device, shape = k_pages.device, k.shape
+    for t in (k, v):
+        if t is not None and (t.dtype is not torch.bfloat16 or t.device != device or t.shape != shape or
+                              len(shape) != 4 or shape[1] != Hkv or shape[3] != d or t.stride(3) != 1):
+            raise ValueError("k and v must be bf16 tensors [B, Hkv, T, d] on the pages' device, last stride 1")
+    B, _, T, _ = shape
+    width = page_table.shape[-1]
+    _check_int("page_table", page_table, device, B, width)
+    _check_int("pos", pos, device, B)
     if count is not None:
-        _check_ints(k.device, count=(count, (B,)))
-    with torch.cuda.device(k.device):
-        rc = lib().attn_pages_append(k.data_ptr(), None if v is None else v.data_ptr(), _strides(k, 0),
-                                     None if v is None else _strides(v, 0), k_pages.data_ptr(),
-                                     None if v is None else v_pages.data_ptr(), strides, page_table.data_ptr(),
-                                     pos.data_ptr(), None if count is None else count.data_ptr(), B, Hkv, T, P,
-                                     page, width, d, _stream_handle(stream))
+        _check_int("count", count, device, B)
+    there = _elsewhere(stream, device)
+    if there is not None:
+        with there:
+            return pages_append(k, v, k_pages, v_pages, page_table, pos, count)
+    if v is None:
+        v_ptr, v_strides, vp_ptr = None, None, None
+    else:
+        v_ptr, v_strides, vp_ptr = v.data_ptr(), _strides(v, 0), v_pages.data_ptr()
+    rc = lib().attn_pages_append(k.data_ptr(), v_ptr, _strides(k, 0), v_strides, k_pages.data_ptr(), vp_ptr, strides,
+                                 page_table.data_ptr(), pos.data_ptr(), None if count is None else count.data_ptr(),
+                                 B, Hkv, T, P, page, width, d, _raw_stream(device))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_pages_append")
 
 
 def pages_workspace_bytes(n: int, num_rows: int, num_pages: int) -> int:
-    r = int(lib().attn_pages_workspace_bytes(int(n), int(num_rows), int(num_pages)))
+    r = lib().attn_pages_workspace_bytes(n, num_rows, num_pages)
     if r < 0:
         raise ValueError("unsupported or invalid shape for the page operations")
     return r
 
 
-def _check_state(device: torch.device, page_table: torch.Tensor, refs: torch.Tensor,
-                 lens: Optional[torch.Tensor] = None, **lists) -> None:
+def _check_state(page_table: torch.Tensor, refs: torch.Tensor, device: torch.device) -> Tuple[int, int, int]:
+    """(num_rows, max_pages, num_pages)."""
     if page_table.dim() != 2 or refs.dim() != 1 or not refs.is_cuda:
         raise ValueError("page_table must be [num_rows, max_pages] and refs a CUDA tensor [num_pages]")
-    _check_ints(device, page_table=(page_table, page_table.shape), refs=(refs, refs.shape))
-    if lens is not None:
-        _check_ints(device, lens=(lens, page_table.shape[:1]))
-    for name, t in lists.items():
-        if t.dim() != 1:
-            raise ValueError(f"{name} must have one dimension")
-        _check_ints(device, **{name: (t, t.shape)})
+    R, width = page_table.shape
+    P = refs.shape[0]
+    _check_int("page_table", page_table, device, R, width)
+    _check_int("refs", refs, device, P)
+    return R, width, P
 
 
 def pages_reserve(page_table: torch.Tensor, refs: torch.Tensor, rows: torch.Tensor, want: torch.Tensor,
@@ -614,22 +629,21 @@ def pages_reserve(page_table: torch.Tensor, refs: torch.Tensor, rows: torch.Tens
     entries below ceil(want / page_size) without a page get the lowest free
     ones (refs 0), whose counts become 1. Returns granted int32 [n]: 1, or 0
     where the free pages did not suffice or the request was not valid."""
-    _check_state(refs.device, page_table, refs, rows=rows, want=want)
-    if rows.shape != want.shape:
-        raise ValueError("rows and want must be alike")
-    n, (R, width), P = rows.shape[0], page_table.shape, refs.shape[0]
+    device, n = refs.device, rows.numel()
+    R, width, P = _check_state(page_table, refs, device)
+    _check_int("rows", rows, device, n)
+    _check_int("want", want, device, n)
+    there = _elsewhere(stream, device)
+    if there is not None:
+        with there:
+            return pages_reserve(page_table, refs, rows, want, page_size, workspace)
     granted = torch.empty_like(rows)
     if n == 0:
         return granted
-    if workspace is None:
-        workspace = _scratch(None, pages_workspace_bytes(n, R, P), refs.device)
-    else:
-        _scratch(workspace, 0, refs.device)
-    with torch.cuda.device(refs.device):
-        rc = lib().attn_pages_reserve(page_table.data_ptr(), refs.data_ptr(), rows.data_ptr(), want.data_ptr(),
-                                      granted.data_ptr(), workspace.data_ptr(),
-                                      workspace.numel() * workspace.element_size(), n, R, P, int(page_size), width,
-                                      _stream_handle(stream))
+    workspace, size = _scratch(workspace, pages_workspace_bytes, (n, R, P), device)
+    rc = lib().attn_pages_reserve(page_table.data_ptr(), refs.data_ptr(), rows.data_ptr(), want.data_ptr(),
+                                  granted.data_ptr(), workspace.data_ptr(), size, n, R, P, page_size, width,
+                                  _raw_stream(device))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_pages_reserve")
     return granted
@@ -644,23 +658,27 @@ def pages_fork(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], page_tabl
     lowest free page. Returns (fresh, granted), int32 [n]: the page taken or
     -1, and 1 or 0. See include/attn.h."""
     Hkv, P, page, d, strides = _pools(k_pages, v_pages)
-    _check_state(k_pages.device, page_table, refs, lens, parents=parents, children=children)
-    if refs.shape[0] != P or parents.shape != children.shape:
-        raise ValueError("refs must have one count a page, and parents and children must be alike")
-    n, (R, width) = parents.shape[0], page_table.shape
-    fresh, granted = torch.empty_like(parents), torch.empty_like(parents)
+    device, n = k_pages.device, parents.numel()
+    R, width, counts = _check_state(page_table, refs, device)
+    if counts != P:
+        raise ValueError("refs must have one count a page")
+    _check_int("lens", lens, device, R)
+    _check_int("parents", parents, device, n)
+    _check_int("children", children, device, n)
+    there = _elsewhere(stream, device)
+    if there is not None:
+        with there:
+            return pages_fork(k_pages, v_pages, page_table, lens, refs, parents, children, workspace)
+    both = torch.empty((2, n), dtype=torch.int32, device=device)
+    fresh, granted = both[0], both[1]
     if n == 0:
         return fresh, granted
-    if workspace is None:
-        workspace = _scratch(None, pages_workspace_bytes(n, R, P), refs.device)
-    else:
-        _scratch(workspace, 0, refs.device)
-    with torch.cuda.device(refs.device):
-        rc = lib().attn_pages_fork(k_pages.data_ptr(), None if v_pages is None else v_pages.data_ptr(), strides,
-                                   page_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), parents.data_ptr(),
-                                   children.data_ptr(), fresh.data_ptr(), granted.data_ptr(), workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), n, R, Hkv, P, page, width, d,
-                                   _stream_handle(stream))
+    workspace, size = _scratch(workspace, pages_workspace_bytes, (n, R, P), device)
+    at = both.data_ptr()
+    rc = lib().attn_pages_fork(k_pages.data_ptr(), None if v_pages is None else v_pages.data_ptr(), strides,
+                               page_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), parents.data_ptr(),
+                               children.data_ptr(), at, at + 4 * n, workspace.data_ptr(), size, n, R, Hkv, P, page,
+                               width, d, _raw_stream(device))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_pages_fork")
     return fresh, granted
@@ -670,13 +688,18 @@ def pages_free(page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
                stream: Optional[torch.cuda.Stream] = None) -> None:
     """Empty rows (int32 [n]) in place: their pages' counts fall, their entries
     become -1 and their lengths 0."""
-    _check_state(refs.device, page_table, refs, lens, rows=rows)
-    n, (R, width) = rows.shape[0], page_table.shape
+    device, n = refs.device, rows.numel()
+    R, width, P = _check_state(page_table, refs, device)
+    _check_int("lens", lens, device, R)
+    _check_int("rows", rows, device, n)
+    there = _elsewhere(stream, device)
+    if there is not None:
+        with there:
+            return pages_free(page_table, lens, refs, rows)
     if n == 0:
         return
-    with torch.cuda.device(refs.device):
-        rc = lib().attn_pages_free(page_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), rows.data_ptr(), n, R,
-                                   refs.shape[0], width, _stream_handle(stream))
+    rc = lib().attn_pages_free(page_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), rows.data_ptr(), n, R, P,
+                               width, _raw_stream(device))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_pages_free")
 
@@ -689,23 +712,23 @@ def pages_compact(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], page_t
     and rename them in the table and the counts: in place, or into ``out``
     (table, refs). Returns the number of live pages, int32 [1] on the device."""
     Hkv, P, page, d, strides = _pools(k_pages, v_pages)
-    _check_state(k_pages.device, page_table, refs)
-    if refs.shape[0] != P:
+    device = k_pages.device
+    R, width, counts = _check_state(page_table, refs, device)
+    if counts != P:
         raise ValueError("refs must have one count a page")
-    R, width = page_table.shape
     table_out, refs_out = (page_table, refs) if out is None else out
-    _check_ints(refs.device, table_out=(table_out, page_table.shape), refs_out=(refs_out, refs.shape))
-    live = torch.empty(1, dtype=torch.int32, device=refs.device)
-    if workspace is None:
-        workspace = _scratch(None, pages_workspace_bytes(0, R, P), refs.device)
-    else:
-        _scratch(workspace, 0, refs.device)
-    with torch.cuda.device(refs.device):
-        rc = lib().attn_pages_compact(k_pages.data_ptr(), None if v_pages is None else v_pages.data_ptr(), strides,
-                                      page_table.data_ptr(), refs.data_ptr(), table_out.data_ptr(),
-                                      refs_out.data_ptr(), live.data_ptr(), workspace.data_ptr(),
-                                      workspace.numel() * workspace.element_size(), R, Hkv, P, page, width, d,
-                                      _stream_handle(stream))
+    _check_int("the table in out", table_out, device, R, width)
+    _check_int("the counts in out", refs_out, device, P)
+    there = _elsewhere(stream, device)
+    if there is not None:
+        with there:
+            return pages_compact(k_pages, v_pages, page_table, refs, out, workspace)
+    live = torch.empty(1, dtype=torch.int32, device=device)
+    workspace, size = _scratch(workspace, pages_workspace_bytes, (0, R, P), device)
+    rc = lib().attn_pages_compact(k_pages.data_ptr(), None if v_pages is None else v_pages.data_ptr(), strides,
+                                  page_table.data_ptr(), refs.data_ptr(), table_out.data_ptr(), refs_out.data_ptr(),
+                                  live.data_ptr(), workspace.data_ptr(), size, R, Hkv, P, page, width, d,
+                                  _raw_stream(device))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_pages_compact")
     return live

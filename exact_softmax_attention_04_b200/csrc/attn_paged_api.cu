@@ -83,10 +83,10 @@ Layout make_layout(int B, int units, int64_t max_tiles, int resident, int nc, in
 {
     Layout l;
     l.units = units;
-    int64_t best = 1, best_waves = 0;
-    for (int64_t r = 1; r <= max_tiles && (r == 1 || (r - 1) * units <= 2 * resident); ++r) {
-        const int64_t waves = (r * units + resident - 1) / resident;
-        if (best_waves == 0 || waves * best < best_waves * r) {
+    int64_t best = 1, best_waves = (units + resident - 1) / resident;
+    for (int64_t waves = 1; waves <= 3; ++waves) {
+        const int64_t r = waves * resident / units < max_tiles ? waves * resident / units : max_tiles;
+        if (r >= 1 && waves * best < best_waves * r) {
             best = r;
             best_waves = waves;
         }
