@@ -47,9 +47,12 @@ struct LatentCfg {
     static_assert(NC == 16 || NC == 32 || NC == 64, "columns");
     static constexpr int GROUPS = NC == 16 ? 1 : 2;            // softmax warpgroups, which share out the columns
     static constexpr int CG = NC / GROUPS;                     // columns of each
-    static constexpr int THREADS = 64 + 128 * GROUPS;
+    static constexpr int THREADS = 96 + 128 * GROUPS;
     static constexpr int BOXES = R / 64 + 1;                   // 64-column boxes per row
     static constexpr int BLOCKS = R / 128;                     // blocks of O^T
+    // A tile's parts, loaded, used and freed one by one: for each block of O^T
+    // its two boxes, and last the box that is no value.
+    static constexpr int PARTS = BLOCKS + 1;
     static constexpr int BOX_BYTES_T = LATENT_TK * 128;        // [64 positions x 64 columns] bf16
     static constexpr int TILE_BYTES = BOXES * BOX_BYTES_T;
     static constexpr int OPB_BOX = NC * 128;                   // NC rows x 64 elements
@@ -62,8 +65,8 @@ struct LatentCfg {
     static constexpr int RED_OFF = P_OFF + P_BYTES;            // fp32 [2][4 warps][NC]
     static constexpr int COL_OFF = RED_OFF + 2 * 4 * NC * 4;   // float2 [NC]: rescaling factor, maximum
     static constexpr int BAR_OFF = COL_OFF + NC * 8;
-    // full[NST], empty[NST], s_full[2], s_free[2], q_full, q_empty, p_full, pv_done, mma_drain
-    static constexpr int NBAR = 2 * NST + 9;
+    // full[NST][PARTS], empty[NST][PARTS], s_full[2], s_free[2], q_full, q_empty, p_full, pv_done, mma_drain[2]
+    static constexpr int NBAR = 2 * NST * PARTS + 10;
     static constexpr int PLAN_OFF = (BAR_OFF + NBAR * 8 + 15) / 16 * 16;
     static constexpr int MISC_OFF = PLAN_OFF + PLAN_SCRATCH;   // TMEM base, abort flag
     // (no slack for alignment: the kernel has no other shared memory, and
@@ -111,12 +114,13 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
     float *const red_all = reinterpret_cast<float *>(smem_raw + C::RED_OFF);
     float2 *const col_all = reinterpret_cast<float2 *>(smem_raw + C::COL_OFF);
     const uint32_t bars = base + C::BAR_OFF;
-    auto full = [&](int st) { return bars + 8u * st; };
-    auto empty = [&](int st) { return bars + 8u * (NST + st); };
-    auto bar1 = [&](int i) { return bars + 8u * (2 * NST + i); };
+    auto full = [&](int st, int part) { return bars + 8u * (st * C::PARTS + part); };
+    auto empty = [&](int st, int part) { return bars + 8u * ((NST + st) * C::PARTS + part); };
+    auto bar1 = [&](int i) { return bars + 8u * (2 * NST * C::PARTS + i); };
     auto s_full = [&](int i) { return bar1(i); };
     auto s_free = [&](int i) { return bar1(2 + i); };
-    const uint32_t q_full = bar1(4), q_empty = bar1(5), p_full = bar1(6), pv_done = bar1(7), mma_drain = bar1(8);
+    const uint32_t q_full = bar1(4), q_empty = bar1(5), p_full = bar1(6), pv_done = bar1(7);
+    auto mma_drain = [&](int i) { return bar1(8 + i); };
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + C::MISC_OFF);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(smem_raw + C::MISC_OFF + 4);
 
@@ -134,10 +138,7 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmC);
-        for (int st = 0; st < NST; ++st) {
-            mbar_init(full(st), 1);
-            mbar_init(empty(st), 1);
-        }
+        for (int i = 0; i < 2 * NST * C::PARTS; ++i) mbar_init(full(0, i), 1);  // full, then empty
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full(i), 1);
             mbar_init(s_free(i), C::GROUPS * 128);
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
         mbar_init(q_empty, 1);
         mbar_init(p_full, C::GROUPS * 128);
         mbar_init(pv_done, 1);
-        mbar_init(mma_drain, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(mma_drain(i), 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -170,14 +171,16 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
         const int page = 1 << p.pages.page_log2;
         const int npg = max(1, LATENT_TK >> p.pages.page_log2);  // pages per tile, one per lane
         const int rows = min(page, LATENT_TK);
-        Walk w;
-        w.start(p.split, run.b, run.j);
+        Walk w = run.walk<LATENT_TK>(p.split);
         auto lane_page = [&]() {
             const int at = w.base() + lane * page;
             return lane < npg ? paged_page(p.split, p.pages, w.s, w.b, npg == 1 ? at & ~(page - 1) : at) : -1;
         };
         int id = lane_page();
         int items = 0, segs = 0;
+        int issued[C::PARTS];  // tiles of which this part was asked for
+#pragma unroll
+        for (int part = 0; part < C::PARTS; ++part) issued[part] = 0;
         bool ok = true;
         for (int i = 0; ok && i < count; ++i) {
             const int cur = id, b = w.b;
@@ -188,22 +191,29 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
                 w.step(p.split);
                 id = lane_page();
             }
-            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, cur >= 0)) * rows * (128 * C::BOXES);
+            const uint32_t have = __ballot_sync(0xffffffffu, cur >= 0);  // pages of the tile that there are
+            const uint32_t bytes = __popc(have) * rows * 128;            // of a box
             const int st = items % NST;
-            if (items >= NST) ok = __all_sync(0xffffffffu, wt.wait(empty(st), ((items / NST) - 1) & 1u));
-            if (!ok) break;
-            if (leader) mbar_arrive_expect_tx(full(st), bytes);
-            __syncwarp();
-            if (cur >= 0) {
-                if (rows == LATENT_TK) {
-                    // one box of all the columns
-                    tma_load_4d(ring(st), &tmC, full(st), 0, row, 0, cur);
-                } else {
-                    for (int bx = 0; bx < C::BOXES; ++bx)
-                        tma_load_4d(ring(st) + bx * C::BOX_BYTES_T + lane * rows * 128, &tmC, full(st), 0, row, bx, cur);
+            // (the part that is no value was freed first)
+#pragma unroll
+            for (int n = 0; n < C::PARTS; ++n) {
+                constexpr int LAST = C::BLOCKS;
+                const int part = n == 0 ? LAST : n - 1, boxes = n == 0 ? 1 : 2;
+                if (items >= NST)
+                    ok = ok && __all_sync(0xffffffffu, wt.wait(empty(st, part), ((items / NST) - 1) & 1u));
+                if (!ok) break;
+                mbar_arrive_expect_tx_if(leader, full(st, part), bytes * boxes);
+                for (int pg = 0; pg < npg; ++pg) {
+                    if (!((have >> pg) & 1u)) continue;
+                    const int page_id = __shfl_sync(0xffffffffu, cur, pg);
+                    const uint32_t dst = ring(st) + 2 * part * C::BOX_BYTES_T + pg * rows * 128;
+                    tma_load_4d_if(leader, dst, &tmC, full(st, part), 0, row, 2 * part, page_id);
+                    if (boxes == 2)
+                        tma_load_4d_if(leader, dst + C::BOX_BYTES_T, &tmC, full(st, part), 0, row, 2 * part + 1, page_id);
                 }
+                issued[part] = items + 1;
             }
-            __syncwarp();
+            if (!ok) break;
             ++items;
             if (starts) {
                 if (segs >= 1) ok = __all_sync(0xffffffffu, wt.wait(q_empty, (segs - 1) & 1u));
@@ -217,52 +227,69 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
             }
         }
         // copies still in flight must land before the CTA exits
-        for (int st = 0; st < NST; ++st) {
-            if (items > st) wt.drain(full(st), ((items - 1 - st) / NST) & 1u);
+#pragma unroll
+        for (int part = 0; part < C::PARTS; ++part) {
+            for (int st = 0; st < NST && st < issued[part]; ++st)
+                wt.drain(full(st, part), ((issued[part] - 1 - st) / NST) & 1u);
         }
         if (segs > 0) wt.drain(q_full, (segs - 1) & 1u);
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
+        // ------------------------------------------------------------ scores' MMAs
         const uint32_t leader = elect_one();
         constexpr uint32_t idesc_s = idesc_bf16_f32(LATENT_TK, NC, 0, 0);  // C, q both K-major
-        constexpr uint32_t idesc_o = idesc_bf16_f32(128, NC, 1, 0);        // C^T MN-major, P^T K-major
         const uint64_t qdesc = smem_desc_sw128(sQ, 16, 1024);
-        const uint64_t pdesc = smem_desc_sw128(sP, 16, 1024);
-        Walk ws, wo;  // where the next scores and the next products are
-        ws.start(p.split, run.b, run.j);
-        wo = ws;
+        Walk w = run.walk<LATENT_TK>(p.split);
         int segs = 0;  // segments whose q has been waited for
-        // Phases are tested one at a time and in order: a barrier is asked about
-        // a phase only when the one before it is known to have completed.
-        auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
-        auto s_ready = [&](int i) {
-            const bool starts = i == 0 || ws.j == 0;
+        bool ok = true;
+        // S(i) = C_i q^T into S buffer i % 2, part by part as they land
+        for (int i = 0; ok && i < count; ++i) {
+            const int st = i % NST;
+            if (i == 0 || w.j == 0) ok = __all_sync(0xffffffffu, wt.wait(q_full, segs++ & 1u));
             // the softmax must have read S(i - 2) out of this buffer
-            return all(mbar_test_wait(full(i % NST), (i / NST) & 1u) &&
-                       (i < 2 || mbar_test_wait(s_free(i % 2), ((i - 2) / 2) & 1u)) &&
-                       (!starts || mbar_test_wait(q_full, segs & 1u)));
-        };
-        // S(i) = C_i q^T into S buffer i % 2
-        auto issue_s = [&](int i) {
-            if (i == 0 || ws.j == 0) ++segs;
-            tc_fence_after();
-            const uint64_t kdesc = smem_desc_sw128(ring(i % NST), 16, 1024);
+            if (ok && i >= 2) ok = __all_sync(0xffffffffu, wt.wait(s_free(i % 2), ((i - 2) / 2) & 1u));
+            const uint64_t kdesc = smem_desc_sw128(ring(st), 16, 1024);
             const uint32_t d_col = tmem + NC * (i % 2);
 #pragma unroll
-            for (int k = 0; k < (R + 64) / 16; ++k) {
-                const uint64_t koff = static_cast<uint64_t>(((k / 4) * C::BOX_BYTES_T + (k % 4) * 32) >> 4);
-                const uint64_t qoff = static_cast<uint64_t>(((k / 4) * C::OPB_BOX + (k % 4) * 32) >> 4);
-                mma_bf16_ss_if(leader, d_col, kdesc + koff, qdesc + qoff, idesc_s, k > 0 ? 1u : 0u);
+            for (int n = 0; n < C::PARTS; ++n) {
+                const int part = n == 0 ? C::BLOCKS : n - 1;
+                ok = ok && __all_sync(0xffffffffu, wt.wait(full(st, part), (i / NST) & 1u));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < (part < C::BLOCKS ? 8 : 4); ++k) {
+                    const int box = 2 * part + k / 4;
+                    const uint64_t koff = static_cast<uint64_t>((box * C::BOX_BYTES_T + (k % 4) * 32) >> 4);
+                    const uint64_t qoff = static_cast<uint64_t>((box * C::OPB_BOX + (k % 4) * 32) >> 4);
+                    mma_bf16_ss_if(leader, d_col, kdesc + koff, qdesc + qoff, idesc_s, n > 0 || k > 0 ? 1u : 0u);
+                }
+                if (n == 0) mma_commit_if(leader, empty(st, part));  // (not read again)
             }
+            if (!ok) break;
             mma_commit_if(leader, s_full(i % 2));
-            if (ws.last()) mma_commit_if(leader, q_empty);
-            if (i + 1 < count) ws.step(p.split);
-        };
-        // O^T += C_i[:, :R]^T P_i^T; a segment's first tile starts from zero
-        auto issue_pv = [&](int i) {
+            if (w.last()) mma_commit_if(leader, q_empty);
+            if (i + 1 < count) w.step(p.split);
+        }
+        // every MMA this warp issued must finish before TMEM is freed
+        mma_commit_if(leader, mma_drain(0));
+        wt.drain(mma_drain(0), 0);
+    } else if (warp == 2 + 4 * C::GROUPS) {
+        // ------------------------------------------------------------ products' MMAs
+        // A warp of their own: S(i + 1) waits for its tile, PV(i) for the
+        // softmax, and neither may hold up the other (PV(i) frees the tile that
+        // the load after next waits for).
+        const uint32_t leader = elect_one();
+        constexpr uint32_t idesc_o = idesc_bf16_f32(128, NC, 1, 0);  // C^T MN-major, P^T K-major
+        const uint64_t pdesc = smem_desc_sw128(sP, 16, 1024);
+        Walk w = run.walk<LATENT_TK>(p.split);
+        // O^T += C_i[:, :R]^T P_i^T by blocks of rows; a segment's first tile
+        // starts from zero
+        for (int i = 0; i < count; ++i) {
+            const int st = i % NST;
+            const uint32_t more = (i == 0 || w.j == 0) ? 0u : 1u;
+            if (i + 1 < count) w.step(p.split);
+            if (!__all_sync(0xffffffffu, wt.wait(p_full, i & 1u))) break;
             tc_fence_after();
-            const uint32_t more = (i == 0 || wo.j == 0) ? 0u : 1u;
-            const uint64_t vdesc = smem_desc_sw128(ring(i % NST), C::BOX_BYTES_T, 1024);
+            const uint64_t vdesc = smem_desc_sw128(ring(st), C::BOX_BYTES_T, 1024);
 #pragma unroll
             for (int blk = 0; blk < C::BLOCKS; ++blk) {
 #pragma unroll
@@ -270,44 +297,12 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
                     mma_bf16_ss_if(leader, tmem + C::O_COL + blk * NC,
                                    vdesc + static_cast<uint64_t>(((2 * blk * C::BOX_BYTES_T) >> 4) + k * 128),
                                    pdesc + static_cast<uint64_t>(k * 2), idesc_o, k > 0 ? 1u : more);
+                mma_commit_if(leader, empty(st, blk));
             }
             mma_commit_if(leader, pv_done);
-            mma_commit_if(leader, empty(i % NST));
-            if (i + 1 < count) wo.step(p.split);
-        };
-        // Whichever is ready: the next scores must not hold up the products,
-        // which free the tile that the load after next waits for.
-        int ns = 0, np = 0;
-        uint64_t since = 0;
-        for (uint32_t spins = 0; np < count; ++spins) {
-            bool did = false;
-            if (ns < count && ns <= np + 1 && s_ready(ns)) {
-                issue_s(ns++);
-                did = true;
-            }
-            if (np < ns && all(mbar_test_wait(p_full, np & 1u))) {
-                issue_pv(np++);
-                did = true;
-            }
-            if (did) {
-                since = 0;
-            } else if ((spins & 63u) == 0 || since == 0) {
-                // give up as Waiter::wait does
-                const uint64_t now = global_timer_ns();
-                if (since == 0) since = now;
-                const bool late = __any_sync(0xffffffffu, now - since > WAIT_LIMIT_NS);
-                if (__any_sync(0xffffffffu, late || *abort_flag)) {
-                    if (leader && late) {
-                        *abort_flag = 1;
-                        atomicOr(p.status, STATUS_WAIT_TIMEOUT);
-                    }
-                    break;
-                }
-            }
         }
-        // every MMA this warp issued must finish before TMEM is freed
-        mma_commit_if(leader, mma_drain);
-        wt.drain(mma_drain, 0);
+        mma_commit_if(leader, mma_drain(1));
+        wt.drain(mma_drain(1), 0);
     } else {
         // ------------------------------------------------------------ softmax
         constexpr int CG = C::CG, NK = CG / 8;      // the group's columns, as blocks of 8
@@ -321,8 +316,7 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
         const float sc = p.scale_log2;
         float *const red = red_all + grp * 8 * CG;  // [2][4 warps][CG]
         float2 *const col_s = col_all + g0;
-        Walk w;
-        w.start(p.split, run.b, run.j);
+        Walk w = run.walk<LATENT_TK>(p.split);
         auto row_page = [&]() {
             return paged_page(p.split, p.pages, w.s, w.b, (w.base() + my_row) & ~((1 << p.pages.page_log2) - 1));
         };
@@ -333,7 +327,10 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
         for (int i = 0; i < count; ++i) {
             const int sb = i % 2, st = i % NST;
             const Walk cur = w;
-            const bool starts = i == 0 || cur.j == 0, ends = i + 1 == count || cur.last();
+            // (by votes, here and below: branches that the compiler knows to be
+            // taken by whole warps)
+            const bool starts = __any_sync(0xffffffffu, i == 0 || cur.j == 0);
+            const bool ends = __any_sync(0xffffffffu, i + 1 == count || cur.last());
             const int len = cur.s.len;
             // Seen by a token at all, and by all of them? Bits by row of the
             // warp's 16.
@@ -363,69 +360,87 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
 #pragma unroll
                 for (int e = 0; e < CG / 2; ++e) s[e] = __uint_as_float(sv[e]) * sc;
                 if (!plain) {
+                    const bool seen0 = (seen_rows >> rr) & 1u, seen1 = (seen_rows >> (rr + 8)) & 1u;
 #pragma unroll
-                    for (int e = 0; e < CG / 2; ++e) {
-                        const int row = rr + ((e & 2) ? 8 : 0), c = c0 + g0 + 8 * (e / 4) + cc + (e & 1);
-                        const int at = cur.base() + 16 * sw + row;
-                        const bool allowed = ((seen_rows >> row) & 1u) && at <= len - T + c % T;
-                        s[e] = allowed ? s[e] : -CUDART_INF_F;
+                    for (int e = 0; e < CG / 2; ++e) s[e] = ((e & 2) ? seen1 : seen0) ? s[e] : -CUDART_INF_F;
+                    if (T > 1) {
+                        // (at = len - T + t: seen by the tokens from t on)
+                        const int t0 = cur.base() + 16 * sw + rr - (len - T);
+#pragma unroll
+                        for (int e = 0; e < CG / 2; ++e) {
+                            const int c = c0 + g0 + 8 * (e / 4) + cc + (e & 1);
+                            s[e] = c % T >= t0 + ((e & 2) ? 8 : 0) ? s[e] : -CUDART_INF_F;
+                        }
                     }
-                }
-#pragma unroll
-                for (int k = 0; k < NK; ++k) {
-                    float a = fmaxf(s[4 * k], s[4 * k + 2]), b = fmaxf(s[4 * k + 1], s[4 * k + 3]);
-#pragma unroll
-                    for (int o = 4; o <= 16; o *= 2) {
-                        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
-                    }
-                    if (lane < 4)
-                        *reinterpret_cast<float2 *>(red + (sb * 4 + sw) * CG + 8 * k + cc) = make_float2(a, b);
                 }
             }
-            // (ok carries a wait that gave up later in the previous tile)
-            ok = named_bar_and(1 + grp, 4 * 32, okw && ok);
-            if (!ok) break;
-            float alpha[CG / 4];
+            // Does a score exceed its column's reference by more than the slack
+            // (or is there none yet)? Rarely but at a segment's start; then the
+            // group takes the tile's maxima.
+            bool above = false;
+            if (okw) {
+#pragma unroll
+                for (int e = 0; e < CG / 2; ++e)
+                    above = above || s[e] > m_run[e / 4 * 2 + (e & 1)] + LATENT_SLACK;
+            }
             bool raised = false;
+            float alpha[CG / 4];
+            // (ok carries a wait that gave up later in the previous tile)
+            if (!__all_sync(0xffffffffu, named_bar_and(1 + grp, 4 * 32, okw && ok && !above))) {
+                if (okw) {
+#pragma unroll
+                    for (int k = 0; k < NK; ++k) {
+                        float a = fmaxf(s[4 * k], s[4 * k + 2]), b = fmaxf(s[4 * k + 1], s[4 * k + 3]);
+#pragma unroll
+                        for (int o = 4; o <= 16; o *= 2) {
+                            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+                            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+                        }
+                        if (lane < 4)
+                            *reinterpret_cast<float2 *>(red + (sb * 4 + sw) * CG + 8 * k + cc) = make_float2(a, b);
+                    }
+                    __syncwarp();
+                }
+                ok = __all_sync(0xffffffffu, named_bar_and(1 + grp, 4 * 32, okw && ok));
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < CG / 4; ++c) {
+                    float tmax = -CUDART_INF_F;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) tmax = fmaxf(tmax, red[(sb * 4 + v) * CG + 8 * (c / 2) + cc + c % 2]);
+                    const bool up = tmax > m_run[c] + LATENT_SLACK;
+                    alpha[c] = up ? ex2_approx(m_run[c] - tmax) : 1.f;
+                    l_part[c] *= alpha[c];
+                    m_run[c] = up ? tmax : m_run[c];
+                    raised = raised || up;
+                }
+                // (a warp's lanes hold every column, with the same values in every warp)
+                raised = __any_sync(0xffffffffu, raised);
+            }
 #pragma unroll
             for (int k = 0; k < NK; ++k) {
-                float2 mx = *reinterpret_cast<const float2 *>(red + sb * 4 * CG + 8 * k + cc);
-#pragma unroll
-                for (int v = 1; v < 4; ++v) {
-                    const float2 t = *reinterpret_cast<const float2 *>(red + (sb * 4 + v) * CG + 8 * k + cc);
-                    mx.x = fmaxf(mx.x, t.x);
-                    mx.y = fmaxf(mx.y, t.y);
-                }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int c = 2 * k + e;
-                    const float tmax = e ? mx.y : mx.x;
-                    // (a column without a position so far has -inf)
-                    const bool up = tmax > m_run[c] + LATENT_SLACK;
-                    const float m_new = up ? tmax : m_run[c];
-                    // measure from 0 while there is none, so that no (-inf) - (-inf) arises
-                    const float m_ref = (m_new == -CUDART_INF_F) ? 0.f : m_new;
-                    alpha[c] = up ? ex2_approx(m_run[c] - m_ref) : 1.f;
+                    // measure from 0 while there is no position, so that no
+                    // (-inf) - (-inf) arises; masked positions give 0
+                    const float m_ref = (m_run[c] == -CUDART_INF_F) ? 0.f : m_run[c];
                     const float p0 = ex2_approx(s[4 * k + e] - m_ref), p1 = ex2_approx(s[4 * k + 2 + e] - m_ref);
                     s[4 * k + e] = p0;
                     s[4 * k + 2 + e] = p1;
-                    l_part[c] = fmaf(l_part[c], alpha[c], p0 + p1);
-                    m_run[c] = m_new;
-                    raised = raised || up;
+                    l_part[c] += p0 + p1;
                 }
             }
             // P^T was last read by PV(i - 1), and O^T then holds the segment's
             // tiles before i
             if (i >= 1) okw = __all_sync(0xffffffffu, wt.wait(pv_done, (i - 1) & 1u));
-            // (a warp's lanes hold every column, with the same values in every warp)
-            raised = __any_sync(0xffffffffu, raised);
             if (raised && !starts) {
                 if (sw == 0 && lane < 4) {
 #pragma unroll
                     for (int c = 0; c < CG / 4; ++c) col_s[8 * (c / 2) + cc + c % 2].x = alpha[c];
                 }
-                okw = named_bar_and(1 + grp, 4 * 32, okw);
+                __syncwarp();
+                okw = __all_sync(0xffffffffu, named_bar_and(1 + grp, 4 * 32, okw));
                 if (okw) {
                     tc_fence_after();
 #pragma unroll 1
@@ -446,13 +461,17 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
             // Positions no token sees may hold anything (see attn_paged_kernel):
             // their values are zeroed, each warp's 16 rows by itself. (S(i), which
             // reads them too, is done.)
-            if (okw && seen_rows != 0xffffu) {
-                okw = __all_sync(0xffffffffu, wt.wait(full(st), (i / NST) & 1u));
-                if (okw && !seen) {
-                    const uint32_t row = ring(st) + my_row * 128;
-                    for (int bx = 2 * grp + lane / 16; bx < R / 64; bx += 2 * C::GROUPS)
+            if (seen_rows != 0xffffu) {
+                // (16-byte chunks in an order that spreads the rows over the banks)
+                const uint32_t row = ring(st) + my_row * 128;
+                for (int blk = grp; okw && blk < C::BLOCKS; blk += C::GROUPS) {
+                    okw = __all_sync(0xffffffffu, wt.wait(full(st, blk), (i / NST) & 1u));
+                    if (okw && !seen) {
+                        const uint32_t box = row + (2 * blk + lane / 16) * C::BOX_BYTES_T;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) st_shared_v4(row + bx * C::BOX_BYTES_T + e * 16, 0u, 0u, 0u, 0u);
+                        for (int e = 0; e < 8; ++e) st_shared_v4(box + ((e ^ (lane & 7)) * 16), 0u, 0u, 0u, 0u);
+                    }
+                    __syncwarp();
                 }
             }
             if (okw) {
@@ -488,54 +507,65 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
                         a += __shfl_xor_sync(0xffffffffu, a, o);
                         b += __shfl_xor_sync(0xffffffffu, b, o);
                     }
-                    if (lane < 4) {
-                        *reinterpret_cast<float2 *>(sums + sw * CG + 8 * k + cc) = make_float2(a, b);
-                        if (sw == 0) {
-                            col_s[8 * k + cc].y = m_run[2 * k];
-                            col_s[8 * k + cc + 1].y = m_run[2 * k + 1];
-                        }
+                    l_part[2 * k] = a;
+                    l_part[2 * k + 1] = b;
+                }
+                if (lane < 4) {
+#pragma unroll
+                    for (int c = 0; c < CG / 4; ++c) {
+                        sums[sw * CG + 8 * (c / 2) + cc + c % 2] = l_part[c];
+                        if (sw == 0) col_s[8 * (c / 2) + cc + c % 2].y = m_run[c];
                     }
                 }
+                __syncwarp();
                 if (ok) ok = __all_sync(0xffffffffu, wt.wait(pv_done, i & 1u));
-                ok = named_bar_and(1 + grp, 4 * 32, ok);
+                ok = __all_sync(0xffffffffu, named_bar_and(1 + grp, 4 * 32, ok));
                 if (!ok) break;
                 tc_fence_after();
                 const int ncol = min(p.GT - c0 - g0, CG);  // the group's columns in use
-                const bool whole = seg_j == 0 && cur.last();
+                const bool whole = __any_sync(0xffffffffu, seg_j == 0 && cur.last());
                 const int64_t row = static_cast<int64_t>(cur.b) * p.GT + c0 + g0;
                 const int64_t slot = paged_slot(blockIdx.x, blockIdx.y, p.split.ranges, cur.b == run.b) * NC + g0;
                 auto sum_of = [&](int c) {
                     return (sums[c] + sums[CG + c]) + (sums[2 * CG + c] + sums[3 * CG + c]);
                 };
-                for (int c = rank_lane; c < ncol; c += 128) {
+                if (rank_lane < CG) {
+                    const int c = rank_lane;
                     const float l = sum_of(c), m = col_s[c].y;
-                    if (whole)
-                        p.lse[row + c] = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
-                    else
+                    if (whole) {
+                        col_s[c].x = l == 0.f ? 0.f : 1.f / l;
+                        if (c < ncol) p.lse[row + c] = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
+                    } else if (c < ncol) {
                         p.part_ml[slot + c] = make_float2(m, l);
+                    }
                 }
+                __syncwarp();
+                named_bar_sync(1 + grp, 4 * 32);
+                // Short loops on purpose: this runs once a segment, and what it
+                // costs is above all fetching its instructions (unrolled over the
+                // columns it took 6.8 us' worth of cycles at 64 columns).
 #pragma unroll 1
-                for (int blk = 0; blk < C::BLOCKS; ++blk) {
-                    const int at = blk * 128 + rank_lane;
-                    uint32_t o[CG];
-                    latent_ld_o<CG>(lane_base + C::O_COL + blk * NC + g0, o);
+                for (int j = 0; j < C::BLOCKS * CG / 8; ++j) {
+                    const int blk = j / (CG / 8), c8 = j % (CG / 8) * 8, at = blk * 128 + rank_lane;
+                    uint32_t o[8];
+                    tmem_ld8(lane_base + C::O_COL + blk * NC + g0 + c8, o);
+                    __nv_bfloat16 *const out = p.o + (row + c8) * R + at;
+                    float *const part = p.part_o + (slot + c8) * R + at;
 #pragma unroll
-                    for (int c = 0; c < CG; ++c) {
-                        if (c < ncol) {
-                            const float v = __uint_as_float(o[c]);
-                            if (whole) {
-                                const float l = sum_of(c);
-                                p.o[(row + c) * R + at] = __float2bfloat16_rn(l == 0.f ? 0.f : v / l);
-                            } else {
-                                p.part_o[(slot + c) * R + at] = v;
-                            }
+                    for (int c = 0; c < 8; ++c) {
+                        const float v = __uint_as_float(o[c]);
+                        if (whole) {
+                            const float x = v * col_s[c8 + c].x;
+                            if (c8 + c < ncol) out[c * R] = __float2bfloat16_rn(x);
+                        } else {
+                            part[c * R] = v;  // (the slot has room for columns not in use)
                         }
                     }
                 }
                 tc_fence_before();
                 // the sums and maxima have been read before the next tile's
                 // maxima, or the next rescaling, overwrite them
-                ok = named_bar_and(1 + grp, 4 * 32, ok);
+                ok = __all_sync(0xffffffffu, named_bar_and(1 + grp, 4 * 32, ok));
                 if (!ok) break;
             }
         }

@@ -254,17 +254,16 @@ struct LatentCall {
     cudaStream_t st;
 };
 
-// A pool as [page][64-column group][token][column]: boxes of a whole tile where
-// a page holds one, else of a page's tokens and 64 columns.
+// A pool as [page][64-column group][token][column]: boxes of a page's tokens
+// (a tile's at most) and 64 columns.
 bool encode_latent(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, const LatentCall &a, int boxes)
 {
-    const bool whole = a.page_size >= attn_sm100::LATENT_TK;
     const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(a.page_size), static_cast<cuuint64_t>(boxes),
                                 static_cast<cuuint64_t>(a.p.pages.num_pages)};
     const cuuint64_t strides[3] = {static_cast<cuuint64_t>(a.token_stride) * 2, 128,
                                    static_cast<cuuint64_t>(a.page_stride) * 2};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(whole ? attn_sm100::LATENT_TK : a.page_size),
-                               static_cast<cuuint32_t>(whole ? boxes : 1), 1};
+    const cuuint32_t rows = a.page_size < attn_sm100::LATENT_TK ? a.page_size : attn_sm100::LATENT_TK;
+    const cuuint32_t box[4] = {64, rows, 1, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(a.pages), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -61,7 +61,8 @@ struct PagedCfg {
     static constexpr int Q_OFF = NST * TILE_BYTES;             // two q buffers
     static constexpr int P_OFF = Q_OFF + 2 * Q_BYTES;          // P^T
     static constexpr int RED_OFF = P_OFF + P_BYTES;            // fp32 [3][NC][4 warps]
-    static constexpr int BAR_OFF = RED_OFF + 3 * 4 * NC * 4;
+    static constexpr int COL_OFF = RED_OFF + 3 * 4 * NC * 4;   // float2 [NC]: reciprocal of the sum, maximum
+    static constexpr int BAR_OFF = COL_OFF + NC * 8;
     // full[NST], empty[NST], q_full[2], q_empty[2], s_full[2], s_free[2], p_full, pv_done, mma_drain
     static constexpr int NBAR = 2 * NST + 11;
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;        // TMEM base, abort flag
@@ -117,6 +118,7 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
     auto sQ = [&](int qb) { return base + C::Q_OFF + qb * C::Q_BYTES; };
     const uint32_t sP = base + C::P_OFF;
     float4 *const red = reinterpret_cast<float4 *>(base_ptr + C::RED_OFF);  // [3][NC]: the four warps
+    float2 *const col_s = reinterpret_cast<float2 *>(base_ptr + C::COL_OFF);
     const uint32_t bars = base + C::BAR_OFF;
     auto full = [&](int st) { return bars + 8u * st; };
     auto empty = [&](int st) { return bars + 8u * (NST + st); };
@@ -187,8 +189,7 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
         const int page = 1 << p.pages.page_log2;
         const int npg = max(1, PAGED_TK >> p.pages.page_log2);  // pages per tile, one per lane
         const int rows = min(page, PAGED_TK);
-        Walk w;
-        w.start(p.split, run.b, run.j);
+        Walk w = run.walk<PAGED_TK>(p.split);
         auto lane_page = [&]() {
             const int at = w.base() + lane * page;
             return lane < npg ? paged_page(p.split, p.pages, w.s, w.b, npg == 1 ? at & ~(page - 1) : at) : -1;
@@ -245,9 +246,8 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
         const uint32_t leader = elect_one();
         constexpr uint32_t idesc_s = idesc_bf16_f32(PAGED_TK, N, 0, 0);  // K, q both K-major
         constexpr uint32_t idesc_o = idesc_bf16_f32(D, N, 1, 0);         // V^T MN-major, P^T K-major
-        Walk ws, wo;  // where the next scores and the next products are
-        ws.start(p.split, run.b, run.j);
-        wo = ws;
+        // where the next scores and the next products are
+        Walk ws = run.walk<PAGED_TK>(p.split), wo = ws;
         int segs = 0;  // segments whose q has been waited for
         // S(i) = K_i q^T into S buffer i % 2
         auto issue_s = [&](int i) -> bool {
@@ -315,8 +315,7 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(sw * 32) << 16);
         const float sc = p.scale_log2;
         const int window = p.split.window;
-        Walk w;
-        w.start(p.split, run.b, run.j);
+        Walk w = run.walk<PAGED_TK>(p.split);
         auto slot_page = [&]() { return paged_page(p.split, p.pages, w.s, w.b, (w.base() + r) & ~((1 << p.pages.page_log2) - 1)); };
         int id = slot_page();
         float m_run[NC], l_part[NC];
@@ -325,7 +324,10 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
         for (int i = 0; i < count; ++i) {
             const int sb = i % 2;
             const Walk cur = w;
-            const bool starts = i == 0 || cur.j == 0, ends = i + 1 == count || cur.last();
+            // (by votes, here and below: branches that the compiler knows to be
+            // taken by whole warps)
+            const bool starts = __any_sync(0xffffffffu, i == 0 || cur.j == 0);
+            const bool ends = __any_sync(0xffffffffu, i + 1 == count || cur.last());
             const int at = cur.base() + r;           // this thread's position
             const int len = cur.s.len;
             // Seen by a token at all, and by all of them? (id >= 0 says that
@@ -359,39 +361,62 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
                     for (int c = 0; c < NC; ++c) s[c] = __uint_as_float(sv[c]) * sc;
                 } else {
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        const int t_u = len - T + (c0 + c) % T;  // the token's position
-                        const bool allowed = seen && at <= t_u && (window < 0 || at >= t_u - window);
-                        s[c] = allowed ? __uint_as_float(sv[c]) * sc : -CUDART_INF_F;
+                    for (int c = 0; c < NC; ++c) s[c] = seen ? __uint_as_float(sv[c]) * sc : -CUDART_INF_F;
+                    if (T > 1) {
+                        // (at = len - T + t: seen by the tokens t .. t + window)
+                        const int t0 = at - (len - T), t1 = window < 0 ? T : t0 + window;
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) {
+                            const int u = (c0 + c) % T;
+                            s[c] = u >= t0 && u <= t1 ? s[c] : -CUDART_INF_F;
+                        }
                     }
                 }
-                float mine = -CUDART_INF_F;  // lane c holds column c's maximum
+            }
+            // Does a score exceed its column's reference by more than the slack
+            // (or is there none yet)? Rarely but at a segment's start; then the
+            // warps take the tile's maxima.
+            bool above = false;
+            if (okw) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) above = above || s[c] > m_run[c] + PAGED_SLACK;
+            }
+            bool raised = false;
+            float alpha[NC];
+            // (ok carries a wait that gave up later in the previous tile)
+            if (!__all_sync(0xffffffffu, named_bar_and(1, 4 * 32, okw && ok && !above))) {
+                if (okw) {
+                    float mine = -CUDART_INF_F;  // lane c holds column c's maximum
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        const float mx = redux_max(s[c]);
+                        mine = lane == c ? mx : mine;
+                    }
+                    if (lane < NC) reinterpret_cast<float *>(&red[sb * NC + lane])[sw] = mine;
+                    __syncwarp();
+                }
+                ok = __all_sync(0xffffffffu, named_bar_and(1, 4 * 32, okw && ok));
+                if (!ok) break;
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
-                    const float mx = redux_max(s[c]);
-                    mine = lane == c ? mx : mine;
+                    const float4 m4 = red[sb * NC + c];
+                    const float tmax = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+                    const bool up = tmax > m_run[c] + PAGED_SLACK;
+                    alpha[c] = up ? ex2_approx(m_run[c] - tmax) : 1.f;
+                    l_part[c] *= alpha[c];
+                    m_run[c] = up ? tmax : m_run[c];
+                    raised = raised || up;
                 }
-                if (lane < NC) reinterpret_cast<float *>(&red[sb * NC + lane])[sw] = mine;
+                raised = __any_sync(0xffffffffu, raised);
             }
-            // (ok carries a wait that gave up later in the previous tile)
-            ok = named_bar_and(1, 4 * 32, okw && ok);
-            if (!ok) break;
-            float pr[NC], alpha[NC];
-            bool raised = false;
+            float pr[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                const float4 m4 = red[sb * NC + c];
-                const float tmax = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-                // (a column without a position so far has -inf)
-                const bool up = tmax > m_run[c] + PAGED_SLACK;
-                const float m_new = up ? tmax : m_run[c];
-                // measure from 0 while there is none, so that no (-inf) - (-inf) arises
-                const float m_ref = (m_new == -CUDART_INF_F) ? 0.f : m_new;
-                alpha[c] = up ? ex2_approx(m_run[c] - m_ref) : 1.f;
-                pr[c] = ex2_approx(s[c] - m_ref);           // 0 for masked positions
-                l_part[c] = fmaf(l_part[c], alpha[c], pr[c]);
-                m_run[c] = m_new;
-                raised = raised || up;
+                // measure from 0 while there is no position, so that no
+                // (-inf) - (-inf) arises; masked positions give 0
+                const float m_ref = (m_run[c] == -CUDART_INF_F) ? 0.f : m_run[c];
+                pr[c] = ex2_approx(s[c] - m_ref);
+                l_part[c] += pr[c];
             }
             // P^T was last read by PV(i - 1), and O^T then holds the segment's
             // tiles before i (every thread decides alike whether to rescale it:
@@ -416,9 +441,10 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
 #pragma unroll
                     for (int bx = 0; bx < C::BOXES; ++bx)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            st_shared_v4(ring(st) + bx * C::BOX_BYTES_T + r * 128 + e * 16, 0u, 0u, 0u, 0u);
+                        for (int e = 0; e < 8; ++e)  // (in an order that spreads the rows over the banks)
+                            st_shared_v4(ring(st) + bx * C::BOX_BYTES_T + r * 128 + ((e ^ (r & 7)) * 16), 0u, 0u, 0u, 0u);
                 }
+                __syncwarp();
             }
             if (okw) {
                 // P^T: row c, column r; rounded to bf16 for the product, as the
@@ -447,36 +473,52 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
                     mine = lane == c ? sum : mine;
                 }
                 if (lane < NC) reinterpret_cast<float *>(&red[2 * NC + lane])[sw] = mine;
+                if (r == 0) {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) col_s[c].y = m_run[c];
+                }
+                __syncwarp();
                 if (ok) ok = __all_sync(0xffffffffu, wt.wait(pv_done, i & 1u));
-                ok = named_bar_and(1, 4 * 32, ok);
+                ok = __all_sync(0xffffffffu, named_bar_and(1, 4 * 32, ok));
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t o[NR];
-                paged_tmem_ld<NC>(lane_base + C::O_COL, o);
-                tc_fence_before();
-                const bool whole = seg_j == 0 && cur.last();
+                const bool whole = __any_sync(0xffffffffu, seg_j == 0 && cur.last());
                 const int64_t row = first_row(cur.b);
                 const int64_t slot = paged_slot(blockIdx.x, blockIdx.y, p.split.ranges, cur.b == run.b) * NC;
+                if (r < NC) {
+                    const float4 l4 = red[2 * NC + r];
+                    const float l = (l4.x + l4.y) + (l4.z + l4.w), m = col_s[r].y;
+                    if (whole) {
+                        col_s[r].x = l == 0.f ? 0.f : 1.f / l;
+                        if (r < ncol) p.lse[row + r] = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
+                    } else {
+                        p.part_ml[slot + r] = make_float2(m, l);
+                    }
+                }
+                __syncwarp();
+                named_bar_sync(1, 4 * 32);
+                // (a short loop: this runs once a segment, and what it costs is
+                // above all fetching its instructions)
+#pragma unroll 1
+                for (int c8 = 0; c8 < NC; c8 += 8) {
+                    uint32_t o[8];
+                    tmem_ld8(lane_base + C::O_COL + c8, o);
+                    __nv_bfloat16 *const out = p.o + (row + c8) * D + dcol;
+                    float *const part = p.part_o + (slot + c8) * D + dcol;
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    if (c < ncol) {
-                        const float4 l4 = red[2 * NC + c];
-                        const float l = (l4.x + l4.y) + (l4.z + l4.w);
+                    for (int c = 0; c < (NC < 8 ? NC : 8); ++c) {
                         const float v = __uint_as_float(o[c]);
                         if (whole) {
-                            if (has_dcol)
-                                p.o[(row + c) * D + dcol] = __float2bfloat16_rn(l == 0.f ? 0.f : v / l);
-                            if (r == c)
-                                p.lse[row + c] = l == 0.f ? -CUDART_INF_F
-                                                          : (m_run[c] + __log2f(l)) * 0.69314718055994531f;
-                        } else {
-                            if (has_dcol) p.part_o[(slot + c) * D + dcol] = v;
-                            if (r == c) p.part_ml[slot + c] = make_float2(m_run[c], l);
+                            const float x = v * col_s[c8 + c].x;
+                            if (has_dcol && c8 + c < ncol) out[c * D] = __float2bfloat16_rn(x);
+                        } else if (has_dcol) {
+                            part[c * D] = v;  // (the slot has room for columns not in use)
                         }
                     }
                 }
-                // (the next segment's sums are written behind the barrier of its
-                // first tile)
+                tc_fence_before();
+                // (the next segment's sums and factors are written behind the
+                // barrier of its first tile)
             }
         }
     }

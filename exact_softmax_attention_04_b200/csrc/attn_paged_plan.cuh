@@ -36,20 +36,33 @@ struct PagedSeq {
 };
 
 template <int TK>
-__device__ __forceinline__ PagedSeq paged_seq(const PagedSplit &p, int b)
+__device__ __forceinline__ PagedSeq paged_seq_of(const PagedSplit &p, int len)
 {
     PagedSeq s;
-    s.len = min(max(__ldg(p.lens + b), 0), p.cap);
+    s.len = min(max(len, 0), p.cap);
     s.first = p.window >= 0 ? max(0, s.len - p.T - p.window) / TK : 0;
     s.ntiles = max(s.len - 1, 0) / TK - s.first + 1;
     return s;
 }
 
-// First tile of run r out of n = min(ranges, total).
-__device__ __forceinline__ int paged_run_start(int total, int r, int n)
+template <int TK>
+__device__ __forceinline__ PagedSeq paged_seq(const PagedSplit &p, int b)
 {
-    return static_cast<int>(static_cast<int64_t>(total) * r / n);
+    return paged_seq_of<TK>(p, __ldg(p.lens + b));
 }
+
+// `total` tiles dealt out to n runs: the first total % n have one more.
+struct PagedDeal {
+    int each, more;
+
+    __device__ __forceinline__ PagedDeal(int total, int n) : each(total / n), more(total % n) {}
+    __device__ __forceinline__ int start(int r) const { return r * each + min(r, more); }
+    __device__ __forceinline__ int run_of(int tile) const
+    {
+        const int large = more * (each + 1);
+        return tile < large ? tile / (each + 1) : more + (tile - large) / each;
+    }
+};
 
 // A place in the order of all tiles: tile j of sequence b.
 template <int TK>
@@ -57,16 +70,14 @@ struct PagedWalk {
     int b, j;
     PagedSeq s;
 
-    __device__ __forceinline__ void start(const PagedSplit &p, int b0, int j0)
-    {
-        b = b0;
-        j = j0;
-        s = paged_seq<TK>(p, b0);
-    }
     // (the caller does not step past the last tile)
     __device__ __forceinline__ void step(const PagedSplit &p)
     {
-        if (++j == s.ntiles) start(p, b + 1, 0);
+        if (++j == s.ntiles) {
+            ++b;
+            j = 0;
+            s = paged_seq<TK>(p, b);
+        }
     }
     __device__ __forceinline__ int base() const { return (s.first + j) * TK; }
     __device__ __forceinline__ bool last() const { return j + 1 == s.ntiles; }
@@ -90,7 +101,13 @@ __device__ __forceinline__ int paged_page(const PagedSplit &p, const PagedTable 
 }
 
 struct PagedRun {
-    int b, j, count;  // first tile, number of tiles (0: none)
+    int b, j, count, len;  // first tile, number of tiles (0: none), the sequence's length
+
+    template <int TK>
+    __device__ __forceinline__ PagedWalk<TK> walk(const PagedSplit &p) const
+    {
+        return {b, j, paged_seq_of<TK>(p, len)};
+    }
 };
 
 // The block's run, for all its NT threads; `scratch`: PLAN_SCRATCH bytes of
@@ -106,8 +123,11 @@ __device__ __forceinline__ PagedRun paged_run(const PagedSplit &p, int r, void *
     const int tid = threadIdx.x, lane = tid % 32;
     const int per = (p.B + NT - 1) / NT;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    int mine = 0;
-    for (int b = b0; b < b1; ++b) mine += paged_seq<TK>(p, b).ntiles;
+    // (the thread's one sequence is read once; with more than NT sequences,
+    // its several are read again)
+    const int len0 = b0 < b1 ? __ldg(p.lens + b0) : 0;
+    int mine = b0 < b1 ? paged_seq_of<TK>(p, len0).ntiles : 0;
+    for (int b = b0 + 1; b < b1; ++b) mine += paged_seq<TK>(p, b).ntiles;
     int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -133,19 +153,20 @@ __device__ __forceinline__ PagedRun paged_run(const PagedSplit &p, int r, void *
     }
     const int n = min(p.ranges, total);
     if (r < n) {
-        const int t0 = paged_run_start(total, r, n);
+        const PagedDeal deal(total, n);
+        const int t0 = deal.start(r);
         int at = upto - mine;
         if (t0 >= at && t0 < upto) {
-            for (int b = b0; b < b1; ++b) {
-                const int tiles = paged_seq<TK>(p, b).ntiles;
-                if (t0 < at + tiles) {
-                    run.b = b;
-                    run.j = t0 - at;
-                    run.count = paged_run_start(total, r + 1, n) - t0;
-                    break;
-                }
+            int b = b0, len = len0, tiles = paged_seq_of<TK>(p, len).ntiles;
+            while (t0 >= at + tiles) {
                 at += tiles;
+                len = __ldg(p.lens + ++b);
+                tiles = paged_seq_of<TK>(p, len).ntiles;
             }
+            run.b = b;
+            run.j = t0 - at;
+            run.len = len;
+            run.count = deal.start(r + 1) - t0;
         }
     }
     __syncthreads();
@@ -227,11 +248,11 @@ __global__ void __launch_bounds__(COMBINE_THREADS) attn_paged_combine_kernel(con
     const int end = before + paged_seq<TK>(p, b).ntiles - 1;  // the last tile
     const int n = min(p.ranges, total);
     // the runs that hold the first and the last tile
-    const int r0 = static_cast<int>(((static_cast<int64_t>(before) + 1) * n - 1) / total);
-    const int r1 = static_cast<int>(((static_cast<int64_t>(end) + 1) * n - 1) / total);
+    const PagedDeal deal(total, n);
+    const int r0 = deal.run_of(before), r1 = deal.run_of(end);
     const int nseg = r1 - r0 + 1;
     // run r0 may begin before the sequence; then this is its last segment
-    const bool r0_first = paged_run_start(total, r0, n) >= before;
+    const bool r0_first = deal.start(r0) >= before;
     auto slot = [&](int s, int c) { return paged_slot(r0 + s, y, p.ranges, s > 0 || r0_first) * NC + c; };
     const int g = tid / LANES, e = tid % LANES;
     const int64_t row0 = (static_cast<int64_t>(b) * a.H + head * G) * p.T + c0;
