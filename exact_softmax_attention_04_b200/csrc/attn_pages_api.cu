@@ -44,6 +44,37 @@ int check_pools(PagePools *p, const void *k_pages, const void *v_pages, const in
     return ATTN_OK;
 }
 
+// A page as the copies see it (see PageShape).
+PageShape page_shape(const PagePools &p)
+{
+    PageShape g;
+    const bool side_by_side = p.heads == 1 || p.head_stride == p.vecs;
+    g.parts = side_by_side ? 1 : p.heads;
+    g.part_stride = p.head_stride;
+    g.row_stride = p.token_stride;
+    g.row = FastDiv(static_cast<uint32_t>(side_by_side ? p.heads * p.vecs : p.vecs));
+    return g;
+}
+
+// A kernel that may start while the one before it in the stream still runs (it
+// waits for its results itself).
+template <class... Params>
+int launch_behind(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t st, const Params &...params)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, params...) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+constexpr int kSMs = 148;
+
 int check_ints(std::initializer_list<const void *> ptrs)
 {
     for (const void *p : ptrs)
@@ -81,6 +112,7 @@ extern "C" int attn_pages_append(const void *k, const void *v, const int64_t *k_
     rc = check_ints({page_table, pos});
     if (rc != ATTN_OK || !aligned(count, 4)) return ATTN_ERR_INVALID;
     if (B > 65535 || static_cast<int64_t>(Hkv) * T > INT_MAX / d) return ATTN_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(Hkv) * a.p.vecs > 65535 * 32 * APPEND_COLS) return ATTN_ERR_UNSUPPORTED;
     const int64_t packed[3] = {static_cast<int64_t>(Hkv) * T * d, static_cast<int64_t>(T) * d, d};
     for (int i = 0; i < 2; ++i) {
         const int64_t *s = i == 0 ? k_strides : v_strides;
@@ -97,9 +129,22 @@ extern "C" int attn_pages_append(const void *k, const void *v, const int64_t *k_
     a.count = count;
     a.T = T;
     a.max_pages = max_pages;
-    const int per = std::max(1, 4 * APPEND_THREADS / (a.p.heads * a.p.vecs));
-    const dim3 grid(static_cast<unsigned>((T + per - 1) / per), static_cast<unsigned>(B));
-    pages_append_kernel<<<grid, APPEND_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(a, per);
+    a.vecs = FastDiv(static_cast<uint32_t>(a.p.vecs));
+    a.page = FastDiv(static_cast<uint32_t>(page_size));
+    // two tokens a warp where that leaves every SM's warps some
+    const int tok = static_cast<int64_t>(B) * T >= 2 * 64 * kSMs ? 2 : 1;
+    const int tokens = tok * (APPEND_THREADS / 32), units = 32 * APPEND_COLS;
+    const dim3 grid(static_cast<unsigned>((T + tokens - 1) / tokens), static_cast<unsigned>(B),
+                    static_cast<unsigned>((Hkv * a.p.vecs + units - 1) / units));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (tok == 2 && v)
+        pages_append_kernel<2, 2><<<grid, APPEND_THREADS, 0, st>>>(a);
+    else if (tok == 2)
+        pages_append_kernel<2, 1><<<grid, APPEND_THREADS, 0, st>>>(a);
+    else if (v)
+        pages_append_kernel<1, 2><<<grid, APPEND_THREADS, 0, st>>>(a);
+    else
+        pages_append_kernel<1, 1><<<grid, APPEND_THREADS, 0, st>>>(a);
     return launched();
 }
 
@@ -118,13 +163,23 @@ extern "C" int attn_pages_reserve(int *page_table, int *refs, const int *rows, c
     a.want = want;
     a.granted = granted;
     a.owner = static_cast<int *>(workspace);
-    a.first = a.owner + num_rows;
+    a.need = a.owner + num_rows;
+    a.first = a.need + n;
     a.list = a.first + n;
     a.n = n;
     a.num_pages = num_pages;
     a.page_size = page_size;
-    pages_reserve_kernel<<<1, PLAN_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return launched();
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (n <= RESERVE_FEW) {
+        pages_reserve_kernel<<<1, PLAN_THREADS, 0, st>>>(a);
+        return launched();
+    }
+    const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(n) * 32 + RESERVE_THREADS - 1) / RESERVE_THREADS);
+    pages_reserve_count_kernel<<<blocks, RESERVE_THREADS, 0, st>>>(a);
+    int rc = launched();
+    if (rc == ATTN_OK) rc = launch_behind(pages_reserve_kernel, dim3(1), PLAN_THREADS, st, a);
+    if (rc == ATTN_OK) rc = launch_behind(pages_reserve_fill_kernel, dim3(blocks), RESERVE_THREADS, st, a);
+    return rc;
 }
 
 extern "C" int attn_pages_fork(void *k_pages, void *v_pages, const int64_t *kv_strides, int *page_table, int *lens,
@@ -140,6 +195,7 @@ extern "C" int attn_pages_fork(void *k_pages, void *v_pages, const int64_t *kv_s
     if (check_ints({page_table, lens, refs, parents, children, fresh, granted, workspace}) != ATTN_OK)
         return ATTN_ERR_INVALID;
     if (workspace_bytes < static_cast<size_t>(4 * workspace_ints(n, num_rows, num_pages))) return ATTN_ERR_INVALID;
+    a.g = page_shape(a.p);
     a.t = {page_table, lens, refs, num_rows, max_pages};
     a.parents = parents;
     a.children = children;
@@ -152,10 +208,10 @@ extern "C" int attn_pages_fork(void *k_pages, void *v_pages, const int64_t *kv_s
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     pages_fork_plan_kernel<<<1, PLAN_THREADS, 0, st>>>(a);
     if (launched() != ATTN_OK) return ATTN_ERR_CUDA;
-    const int64_t units = static_cast<int64_t>(a.p.npools) * Hkv * page_size * a.p.vecs;
-    const unsigned split = static_cast<unsigned>(std::min<int64_t>(64, (units + 1023) / 1024));
-    pages_fork_kernel<<<dim3(static_cast<unsigned>(n), split), FORK_THREADS, 0, st>>>(a);
-    return launched();
+    // eight blocks an SM in all, each with a share of a fork's copy
+    const int split = std::max(1, std::min(8 * kSMs / n, 64));
+    return launch_behind(pages_fork_kernel, dim3(static_cast<unsigned>(n), static_cast<unsigned>(split)), COPY_THREADS,
+                         st, a);
 }
 
 extern "C" int attn_pages_free(int *page_table, int *lens, int *refs, const int *rows, int n, int num_rows,
@@ -181,6 +237,7 @@ extern "C" int attn_pages_compact(void *k_pages, void *v_pages, const int64_t *k
     if (num_rows <= 0 || max_pages <= 0) return ATTN_ERR_INVALID;
     if (check_ints({page_table, refs, table_out, refs_out, live, workspace}) != ATTN_OK) return ATTN_ERR_INVALID;
     if (workspace_bytes < static_cast<size_t>(4 * workspace_ints(0, num_rows, num_pages))) return ATTN_ERR_INVALID;
+    a.g = page_shape(a.p);
     a.table = page_table;
     a.refs = refs;
     a.table_out = table_out;
@@ -194,6 +251,5 @@ extern "C" int attn_pages_compact(void *k_pages, void *v_pages, const int64_t *k
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     pages_compact_plan_kernel<<<1, PLAN_THREADS, 0, st>>>(a);
     if (launched() != ATTN_OK) return ATTN_ERR_CUDA;
-    pages_compact_kernel<<<148 * 8, COMPACT_THREADS, 0, st>>>(a);
-    return launched();
+    return launch_behind(pages_compact_kernel, dim3(8 * kSMs), COPY_THREADS, st, a);
 }

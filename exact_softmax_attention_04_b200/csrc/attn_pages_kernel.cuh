@@ -14,7 +14,24 @@
 #pragma once
 #include <cstdint>
 
+#include "sm100.cuh"
+
 namespace attn_sm100 {
+
+// n / d for n below 2^31 by a multiplication: with s = ceil(log2 d) and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(m, n) + n) >> s (Granlund
+// and Montgomery, division by invariant integers; the sum stays below 2^32).
+struct FastDiv {
+    uint32_t d, m, s;
+
+    __host__ __device__ FastDiv() : d(1), m(1), s(0) {}
+    explicit FastDiv(uint32_t by) : d(by), m(1), s(0)
+    {
+        while ((1ull << s) < d) ++s;
+        m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
+};
 
 // One or two pools of one layout. Strides in 16-byte units.
 struct PagePools {
@@ -27,12 +44,49 @@ struct PagePools {
     int page_size;
 };
 
+// How the copies see a page: `parts` blocks `part_stride` apart, each of rows
+// (tokens) of `row` units `row_stride` apart. Heads are the parts, unless they
+// lie side by side in a token's row (then there is one part).
+struct PageShape {
+    int parts;
+    int64_t part_stride, row_stride;
+    FastDiv row;
+};
+
 struct PageTables {
     int *table;     // [num_rows, max_pages]
     int *lens;      // [num_rows]
     int *refs;      // [num_pages]
     int num_rows, max_pages;
 };
+
+// Units [at, end) of a part, counted row after row, from src to dst by THREADS
+// threads with UNROLL loads in flight each (one at a time, a copy ran at half
+// the memory's rate).
+constexpr int COPY_THREADS = 256;
+
+template <int THREADS, int UNROLL>
+__device__ __forceinline__ void copy_units(uint4 *dst, const uint4 *src, const PageShape &g, int at, int end, int tid)
+{
+    const bool dense = g.row_stride == g.row.d;
+    for (int e = at + tid; e < end; e += THREADS * UNROLL) {
+        uint4 v[UNROLL];
+        int64_t off[UNROLL];
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i) {
+            const int n = e + i * THREADS;
+            off[i] = n;
+            if (!dense) {
+                const uint32_t r = g.row.div(n);
+                off[i] = r * g.row_stride + (n - r * g.row.d);
+            }
+            if (n < end) v[i] = src[off[i]];
+        }
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i)
+            if (e + i * THREADS < end) dst[off[i]] = v[i];
+    }
+}
 
 // ------------------------------------------------------------------- append
 
@@ -44,39 +98,65 @@ struct AppendParams {
     const int *pos;               // [B]
     const int *count;             // [B] or null
     int T, max_pages;
+    FastDiv vecs, page;
 };
 
 constexpr int APPEND_THREADS = 256;
+constexpr int APPEND_COLS = 4;  // 16-byte units a lane takes of a token's row
 
-// New token u of sequence b goes to position pos[b] + u. A block takes
-// `tokens_per_block` tokens of one sequence; a thread keeps its 16-byte column
-// of a token's heads * d row and walks the tokens, so the only divisions in
-// the loop are those by the page size.
-__global__ void __launch_bounds__(APPEND_THREADS) pages_append_kernel(const AppendParams a, int tokens_per_block)
+// New token u of sequence b goes to position pos[b] + u. A warp takes TOK
+// tokens of one sequence (blockIdx.x) and 128 units of their heads * d rows
+// (blockIdx.z): all its loads are issued before the table's answer is waited
+// for, and then the stores.
+template <int TOK, int POOLS>
+__global__ void __launch_bounds__(APPEND_THREADS) pages_append_kernel(const AppendParams a)
 {
     const PagePools &p = a.p;
-    const int b = blockIdx.y;
-    const int row_vecs = p.heads * p.vecs;
+    const int b = blockIdx.y, lane = threadIdx.x % 32;
+    const int u0 = (blockIdx.x * (APPEND_THREADS / 32) + threadIdx.x / 32) * TOK;
     const int n = a.count ? min(max(a.count[b], 0), a.T) : a.T;
-    const int u0 = blockIdx.x * tokens_per_block;
-    const int u1 = min(u0 + tokens_per_block, n);
-    const int64_t pos = a.pos[b];
-    const int *const table = a.table + static_cast<int64_t>(b) * a.max_pages;
-    for (int i = threadIdx.x; i < row_vecs * (u1 - u0); i += APPEND_THREADS) {
-        const int u = u0 + i / row_vecs, r = i % row_vecs;
-        const int h = r / p.vecs, c = r % p.vecs;
-        const int64_t at = pos + u;
-        if (at < 0 || at >= static_cast<int64_t>(a.max_pages) * p.page_size) continue;
-        const int page = table[at / p.page_size];
+    if (u0 >= n) return;
+    const int64_t first = static_cast<int64_t>(a.pos[b]) + u0;
+    const int row_units = p.heads * p.vecs;
+    uint4 v[TOK][APPEND_COLS][POOLS];
+    int64_t to[APPEND_COLS];
+#pragma unroll
+    for (int i = 0; i < APPEND_COLS; ++i) {
+        const int r = (blockIdx.z * APPEND_COLS + i) * 32 + lane;
+        const int h = a.vecs.div(r), c = r - h * p.vecs;
+        to[i] = r < row_units ? h * p.head_stride + c : -1;
+#pragma unroll
+        for (int t = 0; t < TOK; ++t) {
+#pragma unroll
+            for (int k = 0; k < POOLS; ++k)
+                if (r < row_units && u0 + t < n)
+                    v[t][i][k] = a.src[k][b * a.sb[k] + h * a.sh[k] + (u0 + t) * a.st[k] + c];
+        }
+    }
+    const int64_t cap = static_cast<int64_t>(a.max_pages) * p.page_size;
+#pragma unroll
+    for (int t = 0; t < TOK; ++t) {
+        const int64_t at = first + t;
+        if (u0 + t >= n || at < 0 || at >= cap) continue;
+        const int64_t slot_page = cap <= INT32_MAX ? a.page.div(static_cast<uint32_t>(at)) : at / p.page_size;
+        const int page = a.table[static_cast<int64_t>(b) * a.max_pages + slot_page];
         if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) continue;
-        const int64_t dst = page * p.page_stride + h * p.head_stride + (at % p.page_size) * p.token_stride + c;
-        for (int k = 0; k < p.npools; ++k) p.pool[k][dst] = a.src[k][b * a.sb[k] + h * a.sh[k] + u * a.st[k] + c];
+        const int64_t dst = page * p.page_stride + (at - slot_page * p.page_size) * p.token_stride;
+#pragma unroll
+        for (int i = 0; i < APPEND_COLS; ++i) {
+            if (to[i] < 0) continue;
+#pragma unroll
+            for (int k = 0; k < POOLS; ++k) p.pool[k][dst + to[i]] = v[t][i][k];
+        }
     }
 }
 
 // ----------------------------------------------------------- planning (1 CTA)
 
 constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_WARPS = PLAN_THREADS / 32;
+constexpr int PLAN_PAGES = 8;          // pages a thread looks at in one go
+constexpr int PLAN_SMEM_ROWS = 8192;   // owners of this many rows fit in shared memory
 
 // Inclusive sum over the block of one int per thread; `total` to all threads.
 __device__ __forceinline__ int plan_scan(int v, int *warp_sums, int &total)
@@ -89,20 +169,28 @@ __device__ __forceinline__ int plan_scan(int v, int *warp_sums, int &total)
     }
     if (lane == 31) warp_sums[warp] = v;
     __syncthreads();
-    if (warp == 0) {
-        int s = warp_sums[lane];
+    // every warp sums up the warps for itself
+    int s = warp_sums[lane];
 #pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const int t = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += t;
-        }
-        warp_sums[lane] = s;
+    for (int o = 1; o < 32; o *= 2) {
+        const int t = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += t;
     }
+    total = __shfl_sync(0xffffffffu, s, 31);
+    const int before = __shfl_sync(0xffffffffu, s, warp == 0 ? 0 : warp - 1);
     __syncthreads();
-    if (warp > 0) v += warp_sums[warp - 1];
-    total = warp_sums[31];
-    __syncthreads();
-    return v;
+    return v + (warp == 0 ? 0 : before);
+}
+
+// Which of this thread's PLAN_PAGES pages from `base` on are live, as bits.
+__device__ __forceinline__ uint32_t plan_live(const int *refs, int num_pages, int base)
+{
+    const int at = base + static_cast<int>(threadIdx.x) * PLAN_PAGES;
+    uint32_t live = 0;
+#pragma unroll
+    for (int i = 0; i < PLAN_PAGES; ++i)
+        if (at + i < num_pages && refs[at + i] > 0) live |= 1u << i;
+    return live;
 }
 
 // The lowest `wanted` free pages, ascending, into list[]; returns how many
@@ -110,20 +198,23 @@ __device__ __forceinline__ int plan_scan(int v, int *warp_sums, int &total)
 __device__ __forceinline__ int plan_free_pages(const int *refs, int num_pages, int wanted, int *list, int *warp_sums)
 {
     int found = 0;
-    for (int base = 0; base < num_pages && found < wanted; base += PLAN_THREADS) {
-        const int page = base + threadIdx.x;
-        const int is_free = (page < num_pages && refs[page] <= 0) ? 1 : 0;
+    for (int base = 0; base < num_pages && found < wanted; base += PLAN_THREADS * PLAN_PAGES) {
+        const int at = base + static_cast<int>(threadIdx.x) * PLAN_PAGES;
+        const int have = min(max(num_pages - at, 0), PLAN_PAGES);
+        const uint32_t free = ~plan_live(refs, num_pages, base) & ((1u << have) - 1u);
         int total;
-        const int rank = found + plan_scan(is_free, warp_sums, total) - is_free;
-        if (is_free && rank < wanted) list[rank] = page;
+        int rank = found + plan_scan(__popc(free), warp_sums, total) - __popc(free);
+        for (uint32_t f = free; f && rank < wanted; f &= f - 1) list[rank++] = at + __ffs(f) - 1;
         found += total;
     }
     return min(found, wanted);
 }
 
-// owner[row] = the first request that names the row (num requests: nobody).
-__device__ __forceinline__ void plan_owners(const int *rows, int n, int *owner, int num_rows)
+// owner[row] = the first request that names the row (n: nobody). Kept in
+// shared memory where it fits; returns where.
+__device__ __forceinline__ int *plan_owners(const int *rows, int n, int *scratch, int *owner_s, int num_rows)
 {
+    int *const owner = num_rows <= PLAN_SMEM_ROWS ? owner_s : scratch;
     for (int i = threadIdx.x; i < num_rows; i += PLAN_THREADS) owner[i] = n;
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += PLAN_THREADS) {
@@ -131,6 +222,7 @@ __device__ __forceinline__ void plan_owners(const int *rows, int n, int *owner, 
         if (static_cast<unsigned>(r) < static_cast<unsigned>(num_rows)) atomicMin(&owner[r], i);
     }
     __syncthreads();
+    return owner;
 }
 
 struct ReserveParams {
@@ -139,77 +231,142 @@ struct ReserveParams {
     const int *want;  // [n]: tokens each row needs room for
     int *granted;     // [n]
     int *owner;       // workspace [num_rows]
-    int *first;       // workspace [n]
+    int *need;        // workspace [n]: pages a request asks for, -1: not valid
+    int *first;       // workspace [n]: and asked for before it
     int *list;        // workspace [num_pages]
     int n, num_pages, page_size;
 };
 
-// Entries of row r that a request for `want` tokens has to fill: those below
-// ceil(want / page_size) that hold no page. -1: the request cannot be met.
-__device__ __forceinline__ int reserve_need(const ReserveParams &a, int i)
+// A warp looks at a request's table entries, 32 at a time: `each` is called by
+// all lanes with (entry index, whether the entry is one to fill).
+template <class F>
+__device__ __forceinline__ void reserve_entries(const int *row, int pages, F each)
 {
-    const int r = a.rows[i], want = a.want[i];
-    if (static_cast<unsigned>(r) >= static_cast<unsigned>(a.t.num_rows) || a.owner[r] != i) return -1;
-    if (want <= 0) return 0;
-    const int pages = (want - 1) / a.page_size + 1;
-    if (pages > a.t.max_pages) return -1;
-    const int *const row = a.t.table + static_cast<int64_t>(r) * a.t.max_pages;
-    int need = 0;
-    for (int j = 0; j < pages; ++j) need += row[j] < 0 ? 1 : 0;
-    return need;
+    for (int j0 = 0; j0 < pages; j0 += 32) {
+        const int j = j0 + static_cast<int>(threadIdx.x % 32);
+        each(j, j < pages && row[j] < 0);
+    }
 }
 
-__global__ void __launch_bounds__(PLAN_THREADS) pages_reserve_kernel(const ReserveParams a)
+// What request i asks for: how many of the entries below ceil(want / page_size)
+// hold no page; -1: its row is out of range, or the table too narrow. A warp.
+__device__ __forceinline__ void reserve_count(const ReserveParams &a, int i)
 {
-    __shared__ int warp_sums[32];
-    plan_owners(a.rows, a.n, a.owner, a.t.num_rows);
+    const int r = a.rows[i], want = a.want[i];
+    const int pages = want <= 0 ? 0 : (want - 1) / a.page_size + 1;
+    int need = -1;
+    if (static_cast<unsigned>(r) < static_cast<unsigned>(a.t.num_rows) && pages <= a.t.max_pages) {
+        need = 0;
+        reserve_entries(a.t.table + static_cast<int64_t>(r) * a.t.max_pages, pages,
+                        [&](int, bool fill) { need += __popc(__ballot_sync(0xffffffffu, fill)); });
+    }
+    if (threadIdx.x % 32 == 0) a.need[i] = need;
+}
+
+// Gives request i its pages, if it was granted them. A warp.
+__device__ __forceinline__ void reserve_fill(const ReserveParams &a, int i)
+{
+    const int need = a.need[i], lane = threadIdx.x % 32;
+    if (need <= 0 || !a.granted[i]) return;
+    int *const row = a.t.table + static_cast<int64_t>(a.rows[i]) * a.t.max_pages;
+    int k = a.first[i];
+    reserve_entries(row, (a.want[i] - 1) / a.page_size + 1, [&](int j, bool fill) {
+        const uint32_t fills = __ballot_sync(0xffffffffu, fill);
+        if (fill) {
+            const int page = a.list[k + __popc(fills & ((1u << lane) - 1u))];
+            row[j] = page;
+            a.t.refs[page] = 1;
+        }
+        k += __popc(fills);
+    });
+}
+
+// The middle part, by one block: which requests are met, and where their pages
+// begin in the list of the lowest free ones.
+__device__ __forceinline__ void reserve_plan(const ReserveParams &a, int *warp_sums, int *owner_s)
+{
+    const int *const owner = plan_owners(a.rows, a.n, a.owner, owner_s, a.t.num_rows);
     int64_t before = 0;
     for (int base = 0; base < a.n; base += PLAN_THREADS) {
         const int i = base + threadIdx.x;
-        const int need = i < a.n ? reserve_need(a, i) : -1;
+        int need = i < a.n ? a.need[i] : -1;
+        if (need >= 0 && owner[a.rows[i]] != i) a.need[i] = need = -1;
         int total;
-        // sums beyond the pool stay beyond it
-        const int upto = plan_scan(min(max(need, 0), a.num_pages), warp_sums, total);
-        if (i < a.n) a.first[i] = need < 0 ? -1 : static_cast<int>(min(before + upto - need, int64_t(a.num_pages) + 1));
+        // (a request for more than the pool cannot be met, nor can the ones
+        // behind it: counted as one page more than the pool, the sums stay small)
+        const int ask = min(max(need, 0), a.num_pages + 1);
+        const int upto = plan_scan(ask, warp_sums, total);
+        if (i < a.n) a.first[i] = static_cast<int>(min(before + upto - ask, int64_t(a.num_pages) + 1));
         before += total;
     }
     const int wanted = static_cast<int>(min(before, static_cast<int64_t>(a.num_pages)));
     const int found = plan_free_pages(a.t.refs, a.num_pages, wanted, a.list, warp_sums);
-    __syncthreads();
     for (int i = threadIdx.x; i < a.n; i += PLAN_THREADS) {
-        const int first = a.first[i];
-        const int need = first < 0 ? -1 : reserve_need(a, i);
-        const bool ok = need >= 0 && (need == 0 || first + need <= found);
-        a.granted[i] = ok ? 1 : 0;
-        if (ok && need > 0) {
-            int *const row = a.t.table + static_cast<int64_t>(a.rows[i]) * a.t.max_pages;
-            for (int j = 0, k = first; k < first + need; ++j) {
-                if (row[j] >= 0) continue;
-                const int page = a.list[k++];
-                row[j] = page;
-                a.t.refs[page] = 1;
-            }
-        }
+        const int need = a.need[i], first = a.first[i];
+        a.granted[i] = need >= 0 && (need == 0 || (first <= found && need <= found - first)) ? 1 : 0;
     }
+}
+
+// A block has a warp for each of up to RESERVE_FEW requests and does all of it;
+// with more (a warp would go through several rows, one memory latency after
+// another: 40 us for 512 rows), grids of warps count and fill around the plan.
+constexpr int RESERVE_FEW = PLAN_WARPS;
+
+__global__ void __launch_bounds__(PLAN_THREADS) pages_reserve_kernel(const ReserveParams a)
+{
+    __shared__ int warp_sums[PLAN_WARPS];
+    __shared__ int owner_s[PLAN_SMEM_ROWS];
+    const int warp = threadIdx.x / 32;
+    grid_dependents_launch();
+    if (a.n <= RESERVE_FEW) {
+        if (warp < a.n) reserve_count(a, warp);
+        __syncthreads();
+    } else {
+        grid_dependency_wait();
+    }
+    reserve_plan(a, warp_sums, owner_s);
+    if (a.n <= RESERVE_FEW) {
+        __syncthreads();
+        if (warp < a.n) reserve_fill(a, warp);
+    }
+}
+
+constexpr int RESERVE_THREADS = 256;
+
+__global__ void __launch_bounds__(RESERVE_THREADS) pages_reserve_count_kernel(const ReserveParams a)
+{
+    grid_dependents_launch();
+    const int i = blockIdx.x * (RESERVE_THREADS / 32) + threadIdx.x / 32;
+    if (i < a.n) reserve_count(a, i);
+}
+
+__global__ void __launch_bounds__(RESERVE_THREADS) pages_reserve_fill_kernel(const ReserveParams a)
+{
+    grid_dependency_wait();
+    const int i = blockIdx.x * (RESERVE_THREADS / 32) + threadIdx.x / 32;
+    if (i < a.n) reserve_fill(a, i);
 }
 
 // --------------------------------------------------------------------- fork
 
 struct ForkParams {
     PagePools p;
+    PageShape g;
     PageTables t;
     const int *parents, *children;  // [n]
     int *fresh, *granted;           // [n]
     int *owner;                     // workspace [num_rows]
     int *length;                    // workspace [n]: tokens the child gets, -1: not granted
-    int *list;                      // workspace [n]
+    int *list;                      // workspace [num_pages]
     int n;
 };
 
 __global__ void __launch_bounds__(PLAN_THREADS) pages_fork_plan_kernel(const ForkParams a)
 {
-    __shared__ int warp_sums[32];
-    plan_owners(a.children, a.n, a.owner, a.t.num_rows);
+    __shared__ int warp_sums[PLAN_WARPS];
+    __shared__ int owner_s[PLAN_SMEM_ROWS];
+    grid_dependents_launch();
+    int *const owner = plan_owners(a.children, a.n, a.owner, owner_s, a.t.num_rows);
     const unsigned rows = static_cast<unsigned>(a.t.num_rows);
     int before = 0;
     for (int base = 0; base < a.n; base += PLAN_THREADS) {
@@ -218,7 +375,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) pages_fork_plan_kernel(const For
         if (i < a.n) {
             const int from = a.parents[i], to = a.children[i];
             const bool named = static_cast<unsigned>(from) < rows && static_cast<unsigned>(to) < rows &&
-                               a.owner[to] == i;
+                               owner[to] == i;
             // the child holds nothing yet
             if (named && a.t.lens[to] == 0 && a.t.table[static_cast<int64_t>(to) * a.t.max_pages] < 0) {
                 len = max(a.t.lens[from], 0);
@@ -237,7 +394,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) pages_fork_plan_kernel(const For
         }
         before += total;
     }
-    const int found = plan_free_pages(a.t.refs, a.p.num_pages, before, a.list, warp_sums);
+    const int found = plan_free_pages(a.t.refs, a.p.num_pages, min(before, a.p.num_pages), a.list, warp_sums);
     __syncthreads();
     for (int i = threadIdx.x; i < a.n; i += PLAN_THREADS) {
         const int rank = a.fresh[i];
@@ -250,40 +407,41 @@ __global__ void __launch_bounds__(PLAN_THREADS) pages_fork_plan_kernel(const For
     }
 }
 
-constexpr int FORK_THREADS = 256;
-
-// Fork i: blockIdx.x; its rows are spread over gridDim.y blocks. The first of
-// them also writes the child's table row and length and raises the counts of
-// the shared pages. (Lengths come from the plan: a child's own length may be
-// another fork's source only while it is 0.)
-__global__ void __launch_bounds__(FORK_THREADS) pages_fork_kernel(const ForkParams a)
+// Fork i: blockIdx.x; the copy of its last page is spread over gridDim.y
+// blocks. The first of them also writes the child's table row and length and
+// raises the counts of the shared pages. (Lengths come from the plan: a child's
+// own length may be another fork's source only while it is 0.)
+__global__ void __launch_bounds__(COPY_THREADS) pages_fork_kernel(const ForkParams a)
 {
+    grid_dependency_wait();
     const PagePools &p = a.p;
     const int i = blockIdx.x;
-    const int len = a.length[i];
+    const int len = a.length[i], page = a.fresh[i];
     if (len < 0) return;
     const int full = len / p.page_size, part = len % p.page_size;
     const int *const from = a.t.table + static_cast<int64_t>(a.parents[i]) * a.t.max_pages;
+    if (page >= 0) {
+        const int64_t src = from[full] * p.page_stride, dst = page * p.page_stride;
+        // a warp takes up to 512 units of a (pool, part) pair at a time
+        constexpr int CHUNK = 512;
+        const int units = part * a.g.row.d, spans = p.npools * a.g.parts;
+        const int chunks = (units + CHUNK - 1) / CHUNK;
+        const int warps = gridDim.y * (COPY_THREADS / 32);
+        for (int item = blockIdx.y * (COPY_THREADS / 32) + threadIdx.x / 32; item < spans * chunks; item += warps) {
+            const int span = item / chunks, chunk = item % chunks;
+            uint4 *const pool = p.pool[span / a.g.parts] + span % a.g.parts * a.g.part_stride;
+            copy_units<32, 8>(pool + dst, pool + src, a.g, chunk * CHUNK, min(units, (chunk + 1) * CHUNK), threadIdx.x % 32);
+        }
+    }
     if (blockIdx.y == 0) {
         int *const to = a.t.table + static_cast<int64_t>(a.children[i]) * a.t.max_pages;
-        for (int j = threadIdx.x; j < full; j += FORK_THREADS) {
-            const int page = from[j];
-            to[j] = page;
-            if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) atomicAdd(&a.t.refs[page], 1);
+        for (int j = threadIdx.x; j < full; j += COPY_THREADS) {
+            const int shared = from[j];
+            to[j] = shared;
+            if (static_cast<unsigned>(shared) < static_cast<unsigned>(p.num_pages)) atomicAdd(&a.t.refs[shared], 1);
         }
-        for (int j = full + threadIdx.x; j < a.t.max_pages; j += FORK_THREADS) to[j] = j == full ? a.fresh[i] : -1;
+        for (int j = full + threadIdx.x; j < a.t.max_pages; j += COPY_THREADS) to[j] = j == full ? page : -1;
         if (threadIdx.x == 0) a.t.lens[a.children[i]] = len;
-    }
-    const int page = a.fresh[i];
-    if (page < 0) return;
-    const int64_t src = from[full] * p.page_stride, dst = page * p.page_stride;
-    const int per_head = part * p.vecs;
-    for (int e = blockIdx.y * FORK_THREADS + threadIdx.x; e < p.npools * p.heads * per_head;
-         e += gridDim.y * FORK_THREADS) {
-        const int hp = e / per_head, r = e % per_head;
-        const int64_t at = (hp % p.heads) * p.head_stride + (r / p.vecs) * p.token_stride + r % p.vecs;
-        uint4 *const pool = p.pool[hp / p.heads];
-        pool[dst + at] = pool[src + at];
     }
 }
 
@@ -310,82 +468,130 @@ __global__ void __launch_bounds__(FREE_THREADS) pages_free_kernel(const PageTabl
 // With L live pages, the holes are the free pages below L and the movers the
 // live pages at L or above: equally many. The k-th mover goes to the k-th
 // hole (both ascending). No mover's old place is a hole, so all of them move
-// at once.
+// at once. A page's rank needs one running sum only, of the live pages before
+// it: page - live_before(page) holes come before a hole, and
+// live_before(page) - live_before(L) movers before a mover.
 
 struct CompactParams {
     PagePools p;
+    PageShape g;
     const int *table;
     const int *refs;
     int *table_out, *refs_out;  // may be table and refs themselves
     int *live;                  // [1]
     int *holes;                 // workspace [num_pages]: k-th hole
     int *movers;                // workspace [num_pages]: k-th mover
-    int *rank;                  // workspace [num_pages]: a page's number as a mover, -1: it stays
+    int *rank;                  // workspace [num_pages]: from page L on, a mover's number, or -1
     int *moves;                 // workspace [1]
     int64_t cells;              // num_rows * max_pages
 };
 
+// Live pages as bits, a warp reading 32 in a row: up to 32 words a warp.
+constexpr int COMPACT_STEP = PLAN_THREADS * 32;
+
+__device__ __forceinline__ void compact_bits(const int *refs, int num_pages, int base, int words, uint32_t *bits_s)
+{
+    constexpr int AHEAD = 8;  // loads in flight
+    const int lane = threadIdx.x % 32;
+    if (static_cast<int>(threadIdx.x) >= words) bits_s[threadIdx.x] = 0;
+    for (int w0 = threadIdx.x / 32; w0 < words; w0 += AHEAD * PLAN_WARPS) {
+        int n[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int page = base + (w0 + i * PLAN_WARPS) * 32 + lane;
+            n[i] = w0 + i * PLAN_WARPS < words && page < num_pages ? refs[page] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const uint32_t word = __ballot_sync(0xffffffffu, n[i] > 0);
+            if (lane == 0 && w0 + i * PLAN_WARPS < words) bits_s[w0 + i * PLAN_WARPS] = word;
+        }
+    }
+    __syncthreads();
+}
+
 __global__ void __launch_bounds__(PLAN_THREADS) pages_compact_plan_kernel(const CompactParams a)
 {
-    __shared__ int warp_sums[32];
-    const int P = a.p.num_pages;
-    int live = 0, total;
-    for (int base = 0; base < P; base += PLAN_THREADS) {
-        const int page = base + threadIdx.x;
-        plan_scan((page < P && a.refs[page] > 0) ? 1 : 0, warp_sums, total);
-        live += total;
+    __shared__ int warp_sums[PLAN_WARPS];
+    __shared__ uint32_t bits_s[PLAN_THREADS];
+    __shared__ int first_s[PLAN_THREADS];  // live pages before the word
+    grid_dependents_launch();
+    const int P = a.p.num_pages, lane = threadIdx.x % 32;
+    auto words_at = [&](int base) { return min((P - base + 31) / 32, PLAN_THREADS); };
+    int mine = 0, live, total;
+    for (int base = 0; base < P; base += COMPACT_STEP) {
+        if (base > 0) __syncthreads();
+        compact_bits(a.refs, P, base, words_at(base), bits_s);
+        mine += __popc(bits_s[threadIdx.x]);
     }
-    int holes = 0, movers = 0;
-    for (int base = 0; base < P; base += PLAN_THREADS) {
-        const int page = base + threadIdx.x;
-        const bool is_live = page < P && a.refs[page] > 0;
-        const int hole = (page < live && !is_live) ? 1 : 0, mover = (page >= live && is_live) ? 1 : 0;
-        const int h = holes + plan_scan(hole, warp_sums, total);
-        holes += total;
-        const int m = movers + plan_scan(mover, warp_sums, total);
-        movers += total;
-        if (hole) a.holes[h - 1] = page;
-        if (mover) a.movers[m - 1] = page;
-        if (page < P) a.rank[page] = mover ? m - 1 : -1;
+    plan_scan(mine, warp_sums, live);
+    int before = 0, below = live;  // below: live pages below L (P == L: all)
+    for (int base = 0; base < P; base += COMPACT_STEP) {
+        const int words = words_at(base);
+        if (P > COMPACT_STEP) compact_bits(a.refs, P, base, words, bits_s);
+        const int n = __popc(bits_s[threadIdx.x]);
+        first_s[threadIdx.x] = before + plan_scan(n, warp_sums, total) - n;
+        before += total;
+        __syncthreads();
+        if (live < P && live >= base && live < base + COMPACT_STEP) {
+            const int w = (live - base) / 32;
+            below = first_s[w] + __popc(bits_s[w] & ((1u << (live - base) % 32) - 1u));
+        }
+#pragma unroll 4
+        for (int w = threadIdx.x / 32; w < words; w += PLAN_WARPS) {
+            const int page = base + w * 32 + lane;
+            const uint32_t word = bits_s[w];
+            const bool is_live = (word >> lane) & 1u;
+            const int rank = first_s[w] + __popc(word & ((1u << lane) - 1u));
+            if (page < P) {
+                if (page < live && !is_live) a.holes[page - rank] = page;
+                if (page >= live) {
+                    if (is_live) a.movers[rank - below] = page;
+                    a.rank[page] = is_live ? rank - below : -1;
+                }
+            }
+        }
+        __syncthreads();
     }
     if (threadIdx.x == 0) {
         *a.live = live;
-        *a.moves = movers;
+        *a.moves = live - below;
     }
 }
 
-constexpr int COMPACT_THREADS = 256;
-
-__global__ void __launch_bounds__(COMPACT_THREADS) pages_compact_kernel(const CompactParams a)
+__global__ void __launch_bounds__(COPY_THREADS) pages_compact_kernel(const CompactParams a)
 {
+    grid_dependency_wait();
     const PagePools &p = a.p;
-    const int moves = *a.moves;
-    const int64_t tid = static_cast<int64_t>(blockIdx.x) * COMPACT_THREADS + threadIdx.x;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * COMPACT_THREADS;
+    const int moves = *a.moves, live = *a.live;
+    // pages in chunks, so that the last round of blocks is a short one
+    constexpr int CHUNK = 8 * COPY_THREADS;
+    const int units = a.g.row.d * p.page_size, spans = p.npools * a.g.parts;
+    const int chunks = (units + CHUNK - 1) / CHUNK;
+    const int64_t items = static_cast<int64_t>(moves) * spans * chunks;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int chunk = item % chunks, span = item / chunks % spans, k = item / chunks / spans;
+        uint4 *const pool = p.pool[span / a.g.parts] + span % a.g.parts * a.g.part_stride;
+        copy_units<COPY_THREADS, 4>(pool + a.holes[k] * p.page_stride, pool + a.movers[k] * p.page_stride, a.g,
+                                    chunk * CHUNK, min(units, (chunk + 1) * CHUNK), threadIdx.x);
+    }
+    const int64_t tid = static_cast<int64_t>(blockIdx.x) * COPY_THREADS + threadIdx.x;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * COPY_THREADS;
     for (int64_t i = tid; i < a.cells; i += step) {
         const int page = a.table[i];
-        const int r = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages) ? a.rank[page] : -1;
+        const int r = page >= live && page < p.num_pages ? a.rank[page] : -1;
         a.table_out[i] = r < 0 ? page : a.holes[r];
     }
     // a mover's count goes to its hole; every other page's stays where it is
     // (holes are written by their movers alone)
     for (int64_t i = tid; i < p.num_pages; i += step) {
-        const int r = a.rank[i], n = a.refs[i];
-        if (r >= 0) {
-            a.refs_out[a.holes[r]] = n;
+        const int n = a.refs[i];
+        if (i >= live) {
+            const int r = a.rank[i];
+            if (r >= 0) a.refs_out[a.holes[r]] = n;
             a.refs_out[i] = 0;
-        } else if (n > 0 || i >= *a.live) {
-            a.refs_out[i] = max(n, 0);
-        }
-    }
-    const int per_head = p.page_size * p.vecs, per_page = p.npools * p.heads * per_head;
-    for (int k = blockIdx.x; k < moves; k += gridDim.x) {
-        const int64_t src = a.movers[k] * p.page_stride, dst = a.holes[k] * p.page_stride;
-        for (int e = threadIdx.x; e < per_page; e += COMPACT_THREADS) {
-            const int hp = e / per_head, r = e % per_head;
-            const int64_t at = (hp % p.heads) * p.head_stride + (r / p.vecs) * p.token_stride + r % p.vecs;
-            uint4 *const pool = p.pool[hp / p.heads];
-            pool[dst + at] = pool[src + at];
+        } else if (n > 0) {
+            a.refs_out[i] = n;
         }
     }
 }
