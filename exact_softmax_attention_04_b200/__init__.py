@@ -448,15 +448,24 @@ def _pools(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor]):
     return Hkv, P, page, d, strides
 
 
+def _new(shape: tuple, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    """torch.empty, by the constructor that takes the least time on the host."""
+    strides, step = [], 1
+    for n in reversed(shape):
+        strides.append(step)
+        step *= n
+    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=device)
+
+
 def _outputs(q: torch.Tensor, width: int, out: Optional[torch.Tensor], lse: Optional[torch.Tensor]):
     rows = q.shape[:-1]
     shape = rows + (width,)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(q) if width == q.shape[-1] else _new(shape, torch.bfloat16, q.device)
     elif out.shape != shape or out.dtype is not torch.bfloat16 or not out.is_contiguous() or out.device != q.device:
         raise ValueError(f"out must be a contiguous bf16 tensor {list(shape)} on q's device")
     if lse is None:
-        lse = torch.empty(rows, dtype=torch.float32, device=q.device)
+        lse = _new(rows, torch.float32, q.device)
     elif lse.shape != rows or lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.device != q.device:
         raise ValueError(f"lse must be a contiguous fp32 tensor {list(rows)} on q's device")
     return out, lse
@@ -466,7 +475,7 @@ def _scratch(workspace: Optional[torch.Tensor], need, sizes: tuple, device: torc
     """A workspace and its bytes: the caller's, or one of need(*sizes) bytes."""
     if workspace is None:
         n = need(*sizes)
-        return torch.empty(n, dtype=torch.uint8, device=device), n
+        return torch.empty_strided((n,), (1,), dtype=torch.uint8, device=device), n
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the pages' device")
     return workspace, workspace.nbytes
@@ -669,16 +678,14 @@ def pages_fork(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], page_tabl
     if there is not None:
         with there:
             return pages_fork(k_pages, v_pages, page_table, lens, refs, parents, children, workspace)
-    both = torch.empty((2, n), dtype=torch.int32, device=device)
-    fresh, granted = both[0], both[1]
+    fresh, granted = torch.empty_like(parents), torch.empty_like(children)
     if n == 0:
         return fresh, granted
     workspace, size = _scratch(workspace, pages_workspace_bytes, (n, R, P), device)
-    at = both.data_ptr()
     rc = lib().attn_pages_fork(k_pages.data_ptr(), None if v_pages is None else v_pages.data_ptr(), strides,
                                page_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), parents.data_ptr(),
-                               children.data_ptr(), at, at + 4 * n, workspace.data_ptr(), size, n, R, Hkv, P, page,
-                               width, d, _raw_stream(device))
+                               children.data_ptr(), fresh.data_ptr(), granted.data_ptr(), workspace.data_ptr(), size,
+                               n, R, Hkv, P, page, width, d, _raw_stream(device))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_pages_fork")
     return fresh, granted
@@ -723,7 +730,7 @@ def pages_compact(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], page_t
     if there is not None:
         with there:
             return pages_compact(k_pages, v_pages, page_table, refs, out, workspace)
-    live = torch.empty(1, dtype=torch.int32, device=device)
+    live = torch.empty_strided((1,), (1,), dtype=torch.int32, device=device)
     workspace, size = _scratch(workspace, pages_workspace_bytes, (0, R, P), device)
     rc = lib().attn_pages_compact(k_pages.data_ptr(), None if v_pages is None else v_pages.data_ptr(), strides,
                                   page_table.data_ptr(), refs.data_ptr(), table_out.data_ptr(), refs_out.data_ptr(),
