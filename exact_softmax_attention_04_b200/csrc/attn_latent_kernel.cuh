@@ -51,8 +51,11 @@ struct LatentCfg {
     static constexpr int BOXES = R / 64 + 1;                   // 64-column boxes per row
     static constexpr int BLOCKS = R / 128;                     // blocks of O^T
     // A tile's parts, loaded, used and freed one by one: for each block of O^T
-    // its two boxes, and last the box that is no value.
+    // its two boxes, and last the box that is no value. In a part, eight rows of
+    // its first box are followed by the same rows of the second, so that a page
+    // is one TMA copy a part whatever its size.
     static constexpr int PARTS = BLOCKS + 1;
+    static constexpr int PART_BYTES = 2 * LATENT_TK * 128;
     static constexpr int BOX_BYTES_T = LATENT_TK * 128;        // [64 positions x 64 columns] bf16
     static constexpr int TILE_BYTES = BOXES * BOX_BYTES_T;
     static constexpr int OPB_BOX = NC * 128;                   // NC rows x 64 elements
@@ -102,7 +105,7 @@ __device__ __forceinline__ void latent_ld_o(uint32_t taddr, uint32_t (&r)[W])
 template <int R, int NC>
 __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
     attn_latent_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
-                       const LatentParams p)
+                       const __grid_constant__ CUtensorMap tmLast, const LatentParams p)
 {
     using C = LatentCfg<R, NC>;
     using Walk = PagedWalk<LATENT_TK>;
@@ -135,21 +138,17 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
         if (threadIdx.x == 0) atomicOr(p.status, STATUS_WAIT_TIMEOUT);
         return;
     }
-    if (threadIdx.x == 0) {
-        tma_prefetch_desc(&tmQ);
-        tma_prefetch_desc(&tmC);
-        for (int i = 0; i < 2 * NST * C::PARTS; ++i) mbar_init(full(0, i), 1);  // full, then empty
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(s_full(i), 1);
-            mbar_init(s_free(i), C::GROUPS * 128);
+    if (warp == 0) {
+        // (a barrier a lane: one thread would take half a microsecond for them)
+        for (int i = lane; i < C::NBAR; i += 32) {
+            const uint32_t bar = bars + 8u * i;
+            const bool by_softmax = bar == s_free(0) || bar == s_free(1) || bar == p_full;
+            mbar_init(bar, by_softmax ? C::GROUPS * 128 : 1);
         }
-        mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
-        mbar_init(p_full, C::GROUPS * 128);
-        mbar_init(pv_done, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(mma_drain(i), 1);
-        *abort_flag = 0;
+        if (lane == 0) *abort_flag = 0;
         fence_mbar_init();
+        if (lane < 3) tma_prefetch_desc(lane == 0 ? &tmQ : lane == 1 ? &tmC : &tmLast);
+        __syncwarp();
     }
     if (warp == 1) {
         tmem_alloc(smem_addr(tmem_slot), C::TMEM_COLS);
@@ -206,10 +205,8 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
                 for (int pg = 0; pg < npg; ++pg) {
                     if (!((have >> pg) & 1u)) continue;
                     const int page_id = __shfl_sync(0xffffffffu, cur, pg);
-                    const uint32_t dst = ring(st) + 2 * part * C::BOX_BYTES_T + pg * rows * 128;
-                    tma_load_4d_if(leader, dst, &tmC, full(st, part), 0, row, 2 * part, page_id);
-                    if (boxes == 2)
-                        tma_load_4d_if(leader, dst + C::BOX_BYTES_T, &tmC, full(st, part), 0, row, 2 * part + 1, page_id);
+                    tma_load_5d_if(leader, ring(st) + part * C::PART_BYTES + pg * rows * (128 * boxes), n == 0 ? &tmLast : &tmC,
+                                   full(st, part), 0, 0, 2 * part, row / 8, page_id);
                 }
                 issued[part] = items + 1;
             }
@@ -247,7 +244,7 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
             if (i == 0 || w.j == 0) ok = __all_sync(0xffffffffu, wt.wait(q_full, segs++ & 1u));
             // the softmax must have read S(i - 2) out of this buffer
             if (ok && i >= 2) ok = __all_sync(0xffffffffu, wt.wait(s_free(i % 2), ((i - 2) / 2) & 1u));
-            const uint64_t kdesc = smem_desc_sw128(ring(st), 16, 1024);
+            const uint64_t kdesc = smem_desc_sw128(ring(st), 16, 2048), ldesc = smem_desc_sw128(ring(st), 16, 1024);
             const uint32_t d_col = tmem + NC * (i % 2);
 #pragma unroll
             for (int n = 0; n < C::PARTS; ++n) {
@@ -257,10 +254,9 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < (part < C::BLOCKS ? 8 : 4); ++k) {
-                    const int box = 2 * part + k / 4;
-                    const uint64_t koff = static_cast<uint64_t>((box * C::BOX_BYTES_T + (k % 4) * 32) >> 4);
-                    const uint64_t qoff = static_cast<uint64_t>((box * C::OPB_BOX + (k % 4) * 32) >> 4);
-                    mma_bf16_ss_if(leader, d_col, kdesc + koff, qdesc + qoff, idesc_s, n > 0 || k > 0 ? 1u : 0u);
+                    const uint64_t koff = static_cast<uint64_t>((part * C::PART_BYTES + (k / 4) * 1024 + (k % 4) * 32) >> 4);
+                    const uint64_t qoff = static_cast<uint64_t>(((2 * part + k / 4) * C::OPB_BOX + (k % 4) * 32) >> 4);
+                    mma_bf16_ss_if(leader, d_col, (part < C::BLOCKS ? kdesc : ldesc) + koff, qdesc + qoff, idesc_s, n > 0 || k > 0 ? 1u : 0u);
                 }
                 if (n == 0) mma_commit_if(leader, empty(st, part));  // (not read again)
             }
@@ -289,13 +285,13 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
             if (i + 1 < count) w.step(p.split);
             if (!__all_sync(0xffffffffu, wt.wait(p_full, i & 1u))) break;
             tc_fence_after();
-            const uint64_t vdesc = smem_desc_sw128(ring(st), C::BOX_BYTES_T, 1024);
+            const uint64_t vdesc = smem_desc_sw128(ring(st), 1024, 2048);
 #pragma unroll
             for (int blk = 0; blk < C::BLOCKS; ++blk) {
 #pragma unroll
                 for (int k = 0; k < LATENT_TK / 16; ++k)
                     mma_bf16_ss_if(leader, tmem + C::O_COL + blk * NC,
-                                   vdesc + static_cast<uint64_t>(((2 * blk * C::BOX_BYTES_T) >> 4) + k * 128),
+                                   vdesc + static_cast<uint64_t>((blk * C::PART_BYTES + k * 4096) >> 4),
                                    pdesc + static_cast<uint64_t>(k * 2), idesc_o, k > 0 ? 1u : more);
                 mma_commit_if(leader, empty(st, blk));
             }
@@ -463,11 +459,11 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
             // reads them too, is done.)
             if (seen_rows != 0xffffu) {
                 // (16-byte chunks in an order that spreads the rows over the banks)
-                const uint32_t row = ring(st) + my_row * 128;
+                const uint32_t row = ring(st) + (my_row / 8) * 2048 + (my_row % 8) * 128;
                 for (int blk = grp; okw && blk < C::BLOCKS; blk += C::GROUPS) {
                     okw = __all_sync(0xffffffffu, wt.wait(full(st, blk), (i / NST) & 1u));
                     if (okw && !seen) {
-                        const uint32_t box = row + (2 * blk + lane / 16) * C::BOX_BYTES_T;
+                        const uint32_t box = row + blk * C::PART_BYTES + (lane / 16) * 1024;
 #pragma unroll
                         for (int e = 0; e < 8; ++e) st_shared_v4(box + ((e ^ (lane & 7)) * 16), 0u, 0u, 0u, 0u);
                     }

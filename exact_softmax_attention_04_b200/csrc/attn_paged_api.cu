@@ -254,18 +254,19 @@ struct LatentCall {
     cudaStream_t st;
 };
 
-// A pool as [page][64-column group][token][column]: boxes of a page's tokens
-// (a tile's at most) and 64 columns.
-bool encode_latent(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, const LatentCall &a, int boxes)
+// A pool as [page][8 tokens][64-column group][token of the 8][column]: boxes of
+// a page's tokens (a tile's at most) and `boxes` column groups.
+bool encode_latent(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, const LatentCall &a, int groups, int boxes)
 {
-    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(a.page_size), static_cast<cuuint64_t>(boxes),
+    const cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(groups), static_cast<cuuint64_t>(a.page_size / 8),
                                 static_cast<cuuint64_t>(a.p.pages.num_pages)};
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(a.token_stride) * 2, 128,
+    const cuuint64_t strides[4] = {static_cast<cuuint64_t>(a.token_stride) * 2, 128,
+                                   static_cast<cuuint64_t>(a.token_stride) * 16,
                                    static_cast<cuuint64_t>(a.page_stride) * 2};
-    const cuuint32_t rows = a.page_size < attn_sm100::LATENT_TK ? a.page_size : attn_sm100::LATENT_TK;
-    const cuuint32_t box[4] = {64, rows, 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(a.pages), dims, strides, box, estr,
+    const int rows = a.page_size < attn_sm100::LATENT_TK ? a.page_size : attn_sm100::LATENT_TK;
+    const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(boxes), static_cast<cuuint32_t>(rows / 8), 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(a.pages), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -278,9 +279,11 @@ int launch_latent(LatentCall &a)
     auto enc = encoder();
     if (!enc) return ATTN_ERR_CUDA;
     attn_sm100::LatentParams &p = a.p;
-    CUtensorMap mq, mc;
+    CUtensorMap mq, mc, ml;
     const int rows = p.split.B * p.GT;
-    if (!encode_rows(enc, &mq, a.q, rows, R + 64, NC) || !encode_latent(enc, &mc, a, C::BOXES)) return ATTN_ERR_CUDA;
+    if (!encode_rows(enc, &mq, a.q, rows, R + 64, NC) || !encode_latent(enc, &mc, a, C::BOXES, 2) ||
+        !encode_latent(enc, &ml, a, C::BOXES, 1))
+        return ATTN_ERR_CUDA;
     {
         std::lock_guard<std::mutex> lk(g_mu);
         if (!set[a.dev]) {
@@ -295,7 +298,7 @@ int launch_latent(LatentCall &a)
     p.part_ml = reinterpret_cast<float2 *>(a.workspace + a.l.ml);
     p.part_o = reinterpret_cast<float *>(a.workspace + a.l.o);
     const dim3 grid(static_cast<unsigned>(a.l.ranges), static_cast<unsigned>(a.l.units));
-    attn_sm100::attn_latent_kernel<R, NC><<<grid, C::THREADS, C::SMEM_BYTES, a.st>>>(mq, mc, p);
+    attn_sm100::attn_latent_kernel<R, NC><<<grid, C::THREADS, C::SMEM_BYTES, a.st>>>(mq, mc, ml, p);
     if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
     // a sequence of one tile is never split
     if (p.split.cap <= attn_sm100::LATENT_TK) return ATTN_OK;

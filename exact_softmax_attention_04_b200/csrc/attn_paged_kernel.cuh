@@ -142,25 +142,17 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
     auto first_row = [&](int b) { return (b * p.H + head * G) * T + c0; };
 
     grid_dependents_launch();
-    if (threadIdx.x == 0) {
-        tma_prefetch_desc(&tmQ);
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
-        for (int st = 0; st < NST; ++st) {
-            mbar_init(full(st), 1);
-            mbar_init(empty(st), 1);
+    if (warp == 0) {
+        // (a barrier a lane: one thread would take half a microsecond for them)
+        for (int i = lane; i < C::NBAR; i += 32) {
+            const uint32_t bar = bars + 8u * i;
+            const bool by_softmax = bar == s_free(0) || bar == s_free(1) || bar == p_full;
+            mbar_init(bar, by_softmax ? 4 * 32 : 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full(i), 1);
-            mbar_init(q_empty(i), 1);
-            mbar_init(s_full(i), 1);
-            mbar_init(s_free(i), 4 * 32);
-        }
-        mbar_init(p_full, 4 * 32);
-        mbar_init(pv_done, 1);
-        mbar_init(mma_drain, 1);
-        *abort_flag = 0;
+        if (lane == 0) *abort_flag = 0;
         fence_mbar_init();
+        if (lane < 3) tma_prefetch_desc(lane == 0 ? &tmQ : lane == 1 ? &tmK : &tmV);
+        __syncwarp();
     }
     if (warp == 1) {
         tmem_alloc(smem_addr(tmem_slot), C::TMEM_COLS);

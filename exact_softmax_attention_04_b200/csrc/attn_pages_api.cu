@@ -238,6 +238,11 @@ extern "C" int attn_pages_compact(void *k_pages, void *v_pages, const int64_t *k
     if (check_ints({page_table, refs, table_out, refs_out, live, workspace}) != ATTN_OK) return ATTN_ERR_INVALID;
     if (workspace_bytes < static_cast<size_t>(4 * workspace_ints(0, num_rows, num_pages))) return ATTN_ERR_INVALID;
     a.g = page_shape(a.p);
+    if (a.g.row_stride == a.g.row.d && a.g.parts > 1 && a.p.head_stride == page_size * a.p.token_stride) {
+        a.g.parts = 1;
+        a.g.row_stride = Hkv * a.p.vecs;
+        a.g.row = FastDiv(static_cast<uint32_t>(Hkv * a.p.vecs));
+    }
     a.table = page_table;
     a.refs = refs;
     a.table_out = table_out;

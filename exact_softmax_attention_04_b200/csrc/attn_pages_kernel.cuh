@@ -46,7 +46,8 @@ struct PagePools {
 
 // How the copies see a page: `parts` blocks `part_stride` apart, each of rows
 // (tokens) of `row` units `row_stride` apart. Heads are the parts, unless they
-// lie side by side in a token's row (then there is one part).
+// lie side by side in a token's row, or whole pages without gaps are copied
+// (then there is one part).
 struct PageShape {
     int parts;
     int64_t part_stride, row_stride;
@@ -564,16 +565,18 @@ __global__ void __launch_bounds__(COPY_THREADS) pages_compact_kernel(const Compa
     grid_dependency_wait();
     const PagePools &p = a.p;
     const int moves = *a.moves, live = *a.live;
-    // pages in chunks, so that the last round of blocks is a short one
-    constexpr int CHUNK = 8 * COPY_THREADS;
-    const int units = a.g.row.d * p.page_size, spans = p.npools * a.g.parts;
-    const int chunks = (units + CHUNK - 1) / CHUNK;
-    const int64_t items = static_cast<int64_t>(moves) * spans * chunks;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int chunk = item % chunks, span = item / chunks % spans, k = item / chunks / spans;
+    // a warp takes up to 512 units of a (pool, part) pair at a time
+    constexpr int CHUNK = 512;
+    const uint32_t units = a.g.row.d * p.page_size, spans = p.npools * a.g.parts;
+    const uint32_t chunks = (units + CHUNK - 1) / CHUNK, per_page = spans * chunks;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (COPY_THREADS / 32);
+    for (int64_t item = static_cast<int64_t>(blockIdx.x) * (COPY_THREADS / 32) + threadIdx.x / 32;
+         item < static_cast<int64_t>(moves) * per_page; item += warps) {
+        const uint32_t k = item / per_page, rest = item - static_cast<int64_t>(k) * per_page;
+        const uint32_t span = rest / chunks, chunk = rest - span * chunks;
         uint4 *const pool = p.pool[span / a.g.parts] + span % a.g.parts * a.g.part_stride;
-        copy_units<COPY_THREADS, 4>(pool + a.holes[k] * p.page_stride, pool + a.movers[k] * p.page_stride, a.g,
-                                    chunk * CHUNK, min(units, (chunk + 1) * CHUNK), threadIdx.x);
+        copy_units<32, 8>(pool + a.holes[k] * p.page_stride, pool + a.movers[k] * p.page_stride, a.g, chunk * CHUNK,
+                          min(units, (chunk + 1) * CHUNK), threadIdx.x % 32);
     }
     const int64_t tid = static_cast<int64_t>(blockIdx.x) * COPY_THREADS + threadIdx.x;
     const int64_t step = static_cast<int64_t>(gridDim.x) * COPY_THREADS;

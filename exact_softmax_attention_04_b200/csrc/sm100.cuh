@@ -440,15 +440,15 @@ __device__ __forceinline__ void tma_load_3d_if(uint32_t leader, uint32_t dst, co
         : "memory");
 }
 
-__device__ __forceinline__ void tma_load_4d_if(uint32_t leader, uint32_t dst, const CUtensorMap *map,
-                                               uint32_t bar, int x, int y, int z, int w)
+__device__ __forceinline__ void tma_load_5d_if(uint32_t leader, uint32_t dst, const CUtensorMap *map,
+                                               uint32_t bar, int x, int y, int z, int w, int v)
 {
     asm volatile(
         "{\n\t.reg .pred e;\n\t"
-        "setp.ne.b32 e, %7, 0;\n\t"
-        "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "r"(leader)
+        "setp.ne.b32 e, %8, 0;\n\t"
+        "@e cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar), "r"(leader)
         : "memory");
 }
 
