@@ -132,10 +132,10 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
     const int T = p.split.T;
     const int c0 = blockIdx.y * NC;                  // first column of this block
 
-    grid_dependents_launch();
     if (base % 1024 != 0) {
         // (the operands' swizzle needs it)
         if (threadIdx.x == 0) atomicOr(p.status, STATUS_WAIT_TIMEOUT);
+        grid_dependency_wait();
         return;
     }
     if (warp == 0) {
@@ -155,6 +155,10 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
         tmem_relinquish();
     }
     tc_fence_before();
+    // Nothing of the inputs or the workspace is touched before. (The joining
+    // kernel may start once every block is here: it reads the lengths at once.)
+    grid_dependency_wait();
+    grid_dependents_launch();
     // (synchronises the block)
     const PagedRun run = paged_run<LATENT_TK, C::THREADS>(p.split, blockIdx.x, smem_raw + C::PLAN_OFF);
     tc_fence_after();

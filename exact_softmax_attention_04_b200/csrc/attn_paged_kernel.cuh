@@ -141,7 +141,6 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
     // first q row of sequence b's columns: row c0 of its group
     auto first_row = [&](int b) { return (b * p.H + head * G) * T + c0; };
 
-    grid_dependents_launch();
     if (warp == 0) {
         // (a barrier a lane: one thread would take half a microsecond for them)
         for (int i = lane; i < C::NBAR; i += 32) {
@@ -166,6 +165,10 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
         fence_proxy_async_smem();
     }
     tc_fence_before();
+    // Nothing of the inputs or the workspace is touched before. (The joining
+    // kernel may start once every block is here: it reads the lengths at once.)
+    grid_dependency_wait();
+    grid_dependents_launch();
     // (synchronises the block)
     const PagedRun run = paged_run<PAGED_TK, PAGED_THREADS>(p.split, blockIdx.x, base_ptr + C::PLAN_OFF);
     tc_fence_after();

@@ -45,10 +45,12 @@ __device__ __forceinline__ PagedSeq paged_seq_of(const PagedSplit &p, int len)
     return s;
 }
 
+// (Plain loads of lengths and tables, not read-only ones: the block may have
+// started before the kernel that writes them ended.)
 template <int TK>
 __device__ __forceinline__ PagedSeq paged_seq(const PagedSplit &p, int b)
 {
-    return paged_seq_of<TK>(p, __ldg(p.lens + b));
+    return paged_seq_of<TK>(p, p.lens[b]);
 }
 
 // `total` tiles dealt out to n runs: the first total % n have one more.
@@ -96,7 +98,7 @@ __device__ __forceinline__ int paged_page(const PagedSplit &p, const PagedTable 
 {
     const int lo = p.window >= 0 ? max(0, s.len - p.T - p.window) : 0;
     if (at >= s.len || at + (1 << t.page_log2) <= lo) return -1;
-    const int page = __ldg(t.table + static_cast<int64_t>(b) * t.max_pages + (at >> t.page_log2));
+    const int page = t.table[static_cast<int64_t>(b) * t.max_pages + (at >> t.page_log2)];
     return static_cast<unsigned>(page) < static_cast<unsigned>(t.num_pages) ? page : -1;
 }
 
@@ -125,7 +127,7 @@ __device__ __forceinline__ PagedRun paged_run(const PagedSplit &p, int r, void *
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     // (the thread's one sequence is read once; with more than NT sequences,
     // its several are read again)
-    const int len0 = b0 < b1 ? __ldg(p.lens + b0) : 0;
+    const int len0 = b0 < b1 ? p.lens[b0] : 0;
     int mine = b0 < b1 ? paged_seq_of<TK>(p, len0).ntiles : 0;
     for (int b = b0 + 1; b < b1; ++b) mine += paged_seq<TK>(p, b).ntiles;
     int upto = mine;
@@ -160,7 +162,7 @@ __device__ __forceinline__ PagedRun paged_run(const PagedSplit &p, int r, void *
             int b = b0, len = len0, tiles = paged_seq_of<TK>(p, len).ntiles;
             while (t0 >= at + tiles) {
                 at += tiles;
-                len = __ldg(p.lens + ++b);
+                len = p.lens[++b];
                 tiles = paged_seq_of<TK>(p, len).ntiles;
             }
             run.b = b;
@@ -208,6 +210,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS) attn_paged_combine_kernel(con
     __shared__ int red[2][COMBINE_THREADS / 32];
     __shared__ float4 acc_s[GROUPS][LANES];
     __shared__ float l_s[GROUPS];
+    grid_dependents_launch();
     const PagedSplit &p = a.split;
     const int tid = threadIdx.x;
     const int G = a.H / a.Hkv, GT = G * p.T, units = a.Hkv * a.nblk;

@@ -346,6 +346,67 @@ def test_captured_and_replayed_on_another_stream(gpu, form):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("form", ["paged", "latent"])
+@pytest.mark.parametrize("captured", [False, True])
+def test_steps_follow_on_what_the_kernel_before_wrote(gpu, form, captured):
+    """Lengths, tables, queries and cache rows written by kernels right before
+    each call, ten steps without a synchronisation, one workspace for all."""
+    B, Hkv, G, page, steps = 5, 2, 4, 16, 10
+    d = 128 if form == "paged" else 576
+    Hkv = Hkv if form == "paged" else 1
+    start = [3, 700, 64, 15, 2000]
+    k, v, table, ln, g = make(B, Hkv, page, d, [n + steps for n in start], 21, nan=False)
+    new = [(torch.randn((steps, B, Hkv, 1, d), generator=g, device="cuda")).bfloat16() for _ in range(2)]
+    q = queries(g, steps * B, Hkv * G, 1, d).view(steps, B, Hkv * G, 1, d)
+    first = torch.tensor(start, dtype=torch.int32, device="cuda")
+    cur, pos, tb, qq = torch.empty_like(ln), torch.empty_like(ln), torch.empty_like(table), torch.empty_like(q[0])
+    if form == "paged":
+        need = gpu.decode_paged_workspace_bytes(B, Hkv * G, Hkv, 1, table.shape[1], page, d)
+    else:
+        need = gpu.decode_latent_workspace_bytes(B, G, 1, table.shape[1], page, 512)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    outs = []
+
+    def step(i):
+        tb.copy_(table)
+        qq.copy_(q[i])
+        torch.add(first, i, out=pos)
+        torch.add(first, i + 1, out=cur)
+        if form == "paged":
+            gpu.pages_append(new[0][i], new[1][i], k, v, tb, pos)
+            outs.append(gpu.attn_decode_paged(qq, k, v, tb, cur, workspace=ws))
+        else:
+            gpu.pages_append(new[0][i], None, k[:, 0], None, tb, pos)
+            outs.append(gpu.attn_decode_latent(qq, k[:, 0], tb, cur, 0.05, workspace=ws))
+        tb.fill_(-1)
+        cur.fill_(1)
+
+    if captured:
+        kept = k.clone(), v.clone()
+        step(0)
+        outs.clear()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for i in range(steps):
+                step(i)
+        k.copy_(kept[0])
+        v.copy_(kept[1])
+        graph.replay()
+    else:
+        for i in range(steps):
+            step(i)
+    torch.cuda.synchronize()
+    assert gpu.sync_status() == gpu.ATTN_OK
+    for i, (o, lse) in enumerate(outs):
+        n = first + i + 1
+        if form == "paged":
+            check(o, lse, attention(q[i], k, v, table, n, 1 / math.sqrt(d)))
+        else:
+            check(o, lse, attention(q[i], k, k[..., :512], table, n, 0.05))
+
+
+@pytest.mark.gpu
 def test_paged_offsets_past_32_bits(gpu):
     """A pool of more than 2^32 elements, used at both ends."""
     P, Hkv, page, d = 34000, 8, 128, 128
