@@ -89,6 +89,15 @@ __device__ __forceinline__ void copy_units(uint4 *dst, const uint4 *src, const P
     }
 }
 
+// Every kernel here is launched so that it may start while the one before it
+// in the stream still runs: it waits for that one first, and lets the next one
+// do the same. (Then a call's launches cost about a microsecond less each.)
+__device__ __forceinline__ void begin_behind()
+{
+    grid_dependency_wait();
+    grid_dependents_launch();
+}
+
 // ------------------------------------------------------------------- append
 
 struct AppendParams {
@@ -112,6 +121,7 @@ constexpr int APPEND_COLS = 4;  // 16-byte units a lane takes of a token's row
 template <int TOK, int POOLS>
 __global__ void __launch_bounds__(APPEND_THREADS) pages_append_kernel(const AppendParams a)
 {
+    begin_behind();
     const PagePools &p = a.p;
     const int b = blockIdx.y, lane = threadIdx.x % 32;
     const int u0 = (blockIdx.x * (APPEND_THREADS / 32) + threadIdx.x / 32) * TOK;
@@ -318,12 +328,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) pages_reserve_kernel(const Reser
     __shared__ int warp_sums[PLAN_WARPS];
     __shared__ int owner_s[PLAN_SMEM_ROWS];
     const int warp = threadIdx.x / 32;
-    grid_dependents_launch();
+    begin_behind();
     if (a.n <= RESERVE_FEW) {
         if (warp < a.n) reserve_count(a, warp);
         __syncthreads();
-    } else {
-        grid_dependency_wait();
     }
     reserve_plan(a, warp_sums, owner_s);
     if (a.n <= RESERVE_FEW) {
@@ -336,14 +344,14 @@ constexpr int RESERVE_THREADS = 256;
 
 __global__ void __launch_bounds__(RESERVE_THREADS) pages_reserve_count_kernel(const ReserveParams a)
 {
-    grid_dependents_launch();
+    begin_behind();
     const int i = blockIdx.x * (RESERVE_THREADS / 32) + threadIdx.x / 32;
     if (i < a.n) reserve_count(a, i);
 }
 
 __global__ void __launch_bounds__(RESERVE_THREADS) pages_reserve_fill_kernel(const ReserveParams a)
 {
-    grid_dependency_wait();
+    begin_behind();
     const int i = blockIdx.x * (RESERVE_THREADS / 32) + threadIdx.x / 32;
     if (i < a.n) reserve_fill(a, i);
 }
@@ -366,7 +374,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) pages_fork_plan_kernel(const For
 {
     __shared__ int warp_sums[PLAN_WARPS];
     __shared__ int owner_s[PLAN_SMEM_ROWS];
-    grid_dependents_launch();
+    begin_behind();
     int *const owner = plan_owners(a.children, a.n, a.owner, owner_s, a.t.num_rows);
     const unsigned rows = static_cast<unsigned>(a.t.num_rows);
     int before = 0;
@@ -414,7 +422,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) pages_fork_plan_kernel(const For
 // own length may be another fork's source only while it is 0.)
 __global__ void __launch_bounds__(COPY_THREADS) pages_fork_kernel(const ForkParams a)
 {
-    grid_dependency_wait();
+    begin_behind();
     const PagePools &p = a.p;
     const int i = blockIdx.x;
     const int len = a.length[i], page = a.fresh[i];
@@ -454,6 +462,7 @@ constexpr int FREE_THREADS = 256;
 // table by an exchange.
 __global__ void __launch_bounds__(FREE_THREADS) pages_free_kernel(const PageTables t, const int *rows, int num_pages)
 {
+    begin_behind();
     const int r = rows[blockIdx.x];
     if (static_cast<unsigned>(r) >= static_cast<unsigned>(t.num_rows)) return;
     int *const row = t.table + static_cast<int64_t>(r) * t.max_pages;
@@ -516,7 +525,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) pages_compact_plan_kernel(const 
     __shared__ int warp_sums[PLAN_WARPS];
     __shared__ uint32_t bits_s[PLAN_THREADS];
     __shared__ int first_s[PLAN_THREADS];  // live pages before the word
-    grid_dependents_launch();
+    begin_behind();
     const int P = a.p.num_pages, lane = threadIdx.x % 32;
     auto words_at = [&](int base) { return min((P - base + 31) / 32, PLAN_THREADS); };
     int mine = 0, live, total;
@@ -562,7 +571,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) pages_compact_plan_kernel(const 
 
 __global__ void __launch_bounds__(COPY_THREADS) pages_compact_kernel(const CompactParams a)
 {
-    grid_dependency_wait();
+    begin_behind();
     const PagePools &p = a.p;
     const int moves = *a.moves, live = *a.live;
     // a warp takes up to 512 units of a (pool, part) pair at a time
