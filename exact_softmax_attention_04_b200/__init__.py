@@ -526,7 +526,7 @@ def attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
     out, lse = _outputs(q, d, out, lse)
     rc = lib().attn_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), strides,
                                  page_table.data_ptr(), lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                 workspace.data_ptr(), size, B, H, Hkv, T, P, page, width, window, d,
+                                 workspace.data_ptr(), size, B, H, Hkv, T, P, page, width, min(window, 1 << 30), d,
                                  1.0 / math.sqrt(d) if scale is None else scale, _raw_stream(q.device))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode_paged")

@@ -116,7 +116,9 @@ int launch_behind(void (*kernel)(Params...), dim3 grid, int threads, int smem, c
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return ATTN_OK;
+    cudaGetLastError();  // (reported here)
+    return ATTN_ERR_CUDA;
 }
 
 template <int TK, int DV, int NC>

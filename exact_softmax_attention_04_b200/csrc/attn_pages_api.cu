@@ -70,7 +70,9 @@ int launch_behind(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return ATTN_OK;
+    cudaGetLastError();  // (reported here)
+    return ATTN_ERR_CUDA;
 }
 
 constexpr int kSMs = 148;
