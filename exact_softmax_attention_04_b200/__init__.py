@@ -2,8 +2,9 @@
 
 Argument marshalling only. Every step of the computation runs in the CUDA
 kernels of ``libattn_b200.so`` (built in-tree by ``build_lib.py``); this module
-checks tensor properties, allocates outputs with torch and passes raw
-pointers and the current CUDA stream through the C ABI of ``include/attn.h``.
+(and, for the paged caches, ``attn_bind.so``) checks tensor properties,
+allocates outputs with torch and passes raw pointers and the current CUDA
+stream through the C ABI of ``include/attn.h``.
 There is no CPU fallback: the first call that needs the library raises if
 it is missing.
 """
@@ -18,6 +19,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libattn_b200.so")
+BIND_PATH = os.path.join(_PKG, "attn_bind.so")
 
 ATTN_OK = 0
 ATTN_ERR_INVALID = 1
@@ -387,112 +389,39 @@ def attn_decode_multi(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
 # ---------------------------------------------------------------------------
 # Paged caches (see "Paged caches" in include/attn.h)
 
-# These calls are made every step and often on little data, so what a call
-# costs on the host counts: tensors are looked at once each, and the current
-# device and stream are switched only if they are not the right ones already.
+# These calls are made every step and often on little data, so they go through
+# attn_bind (csrc/bind.cpp), which checks the tensors, allocates and calls the C
+# ABI on the current stream of the tensors' device.
 
-def _elsewhere(stream: Optional[torch.cuda.Stream], device: torch.device):
-    """None if a call on ``device`` can go to the current stream; else a context
-    in which it can: there, what the call allocates belongs to its stream."""
-    if stream is None:
-        return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-    if stream.device != device:
+_bind_handle = None
+
+
+def _bind():
+    """The binding module (loaded on first use, with the library it calls)."""
+    global _bind_handle
+    if _bind_handle is None:
+        lib()
+        try:
+            from . import attn_bind
+        except ImportError as e:
+            raise ImportError(f"{BIND_PATH} cannot be loaded ({e}): build it with "
+                              "`python -m exact_softmax_attention_04_b200.build_lib`") from e
+        _bind_handle = attn_bind
+    return _bind_handle
+
+
+def _on(stream: torch.cuda.Stream, t: torch.Tensor):
+    """The context in which a call on t's device goes to ``stream``, and what it
+    allocates belongs to it."""
+    if stream.device != t.device:
         raise ValueError("stream must be on the tensors' device")
     return torch.cuda.stream(stream)
 
 
-def _raw_stream(device: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _check_int(name: str, t: torch.Tensor, device: torch.device, *shape: int) -> None:
-    if t.dtype is not torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on the pages' device")
-
-
-def _strides(t: torch.Tensor, at_least: int):
-    """The strides of all dimensions but the last as a C array, None if t is
-    contiguous. A dimension of one element is never stepped along: its stride
-    is given as ``at_least``."""
-    if t.is_contiguous():
-        return None
-    n = t.dim() - 1
-    return (ctypes.c_int64 * n)(*[x if m > 1 else at_least for x, m in zip(t.stride()[:n], t.shape)])
-
-
-def _check_pool(name: str, pool: torch.Tensor) -> None:
-    if pool.dtype is not torch.bfloat16 or not pool.is_cuda:
-        raise ValueError(f"{name} must be a bf16 CUDA tensor")
-    if pool.stride(-1) != 1 and pool.shape[-1] != 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
-
-
-def _pools(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor]):
-    """(Hkv, num_pages, page_size, d, strides) of one or two pools."""
-    _check_pool("k_pages", k_pages)
-    if v_pages is None:
-        if k_pages.dim() == 3:
-            k_pages = k_pages.unsqueeze(1)
-        if k_pages.dim() != 4:
-            raise ValueError("a single pool must be [num_pages, page_size, d] or [num_pages, Hkv, page_size, d]")
-        P, Hkv, page, d = k_pages.shape
-        return Hkv, P, page, d, _strides(k_pages, d)
-    _check_pool("v_pages", v_pages)
-    shape = k_pages.shape
-    if len(shape) != 4 or shape != v_pages.shape or k_pages.device != v_pages.device:
-        raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, d], alike and on one device")
-    P, Hkv, page, d = shape
-    strides, other = _strides(k_pages, d), _strides(v_pages, d)
-    if (strides is None) != (other is None) or (strides is not None and strides[:] != other[:]):
-        raise ValueError("k_pages and v_pages must have the same strides")
-    return Hkv, P, page, d, strides
-
-
-def _new(shape: tuple, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
-    """torch.empty, by the constructor that takes the least time on the host."""
-    strides, step = [], 1
-    for n in reversed(shape):
-        strides.append(step)
-        step *= n
-    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=device)
-
-
-def _outputs(q: torch.Tensor, width: int, out: Optional[torch.Tensor], lse: Optional[torch.Tensor]):
-    rows = q.shape[:-1]
-    shape = rows + (width,)
-    if out is None:
-        out = torch.empty_like(q) if width == q.shape[-1] else _new(shape, torch.bfloat16, q.device)
-    elif out.shape != shape or out.dtype is not torch.bfloat16 or not out.is_contiguous() or out.device != q.device:
-        raise ValueError(f"out must be a contiguous bf16 tensor {list(shape)} on q's device")
-    if lse is None:
-        lse = _new(rows, torch.float32, q.device)
-    elif lse.shape != rows or lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.device != q.device:
-        raise ValueError(f"lse must be a contiguous fp32 tensor {list(rows)} on q's device")
-    return out, lse
-
-
-def _scratch(workspace: Optional[torch.Tensor], need, sizes: tuple, device: torch.device) -> Tuple[torch.Tensor, int]:
-    """A workspace and its bytes: the caller's, or one of need(*sizes) bytes."""
-    if workspace is None:
-        n = need(*sizes)
-        return torch.empty_strided((n,), (1,), dtype=torch.uint8, device=device), n
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the pages' device")
-    return workspace, workspace.nbytes
-
-
-def _check_queries(q: torch.Tensor, pages: torch.Tensor, d: int, page_table: torch.Tensor,
-                   lens: torch.Tensor) -> Tuple[int, int, int, int]:
-    """(B, H, T, max_pages)."""
-    if q.dtype is not torch.bfloat16 or q.device != pages.device or not q.is_contiguous():
-        raise ValueError("q must be a contiguous bf16 tensor on the pages' device")
-    shape, width = q.shape, page_table.shape[-1]
-    if len(shape) not in (3, 4) or shape[-1] != d:
-        raise ValueError("q must be [B, H, T, x] or [B, H, x] with x the length of the pages' rows")
-    B = shape[0]
-    _check_int("page_table", page_table, q.device, B, width)
-    _check_int("lens", lens, q.device, B)
-    return B, shape[1], shape[2] if len(shape) == 4 else 1, width
+def _checked(result, where: str):
+    if result.__class__ is int:
+        raise AttnError(result, where)
+    return result
 
 
 def decode_paged_workspace_bytes(B: int, H: int, Hkv: int, T: int, max_pages: int, page_size: int, d: int) -> int:
@@ -516,21 +445,11 @@ def attn_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
     ones included. window < 0: every earlier position. Returns (o shaped like
     q, lse fp32 without the last dimension); a token that sees no position
     gets 0 and -inf. See include/attn.h."""
-    Hkv, P, page, d, strides = _pools(k_pages, v_pages)
-    B, H, T, width = _check_queries(q, k_pages, d, page_table, lens)
-    there = _elsewhere(stream, q.device)
-    if there is not None:
-        with there:
+    if stream is not None:
+        with _on(stream, q):
             return attn_decode_paged(q, k_pages, v_pages, page_table, lens, window, scale, out, lse, workspace)
-    workspace, size = _scratch(workspace, decode_paged_workspace_bytes, (B, H, Hkv, T, width, page, d), q.device)
-    out, lse = _outputs(q, d, out, lse)
-    rc = lib().attn_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), strides,
-                                 page_table.data_ptr(), lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                 workspace.data_ptr(), size, B, H, Hkv, T, P, page, width, min(window, 1 << 30), d,
-                                 1.0 / math.sqrt(d) if scale is None else scale, _raw_stream(q.device))
-    if rc != ATTN_OK:
-        raise AttnError(rc, "attn_decode_paged")
-    return out, lse
+    return _checked(_bind().decode_paged(q, k_pages, v_pages, page_table, lens, window, scale, out, lse, workspace),
+                    "attn_decode_paged")
 
 
 def decode_latent_workspace_bytes(B: int, H: int, T: int, max_pages: int, page_size: int, rank: int) -> int:
@@ -553,25 +472,11 @@ def attn_decode_latent(q: torch.Tensor, pages: torch.Tensor, page_table: torch.T
     of a row are the values of every head. ``scale`` is the expanded heads' own
     (rank does not tell it). Returns (o [B, H, T, rank] or [B, H, rank], lse
     fp32). See include/attn.h."""
-    Hkv, P, page, D, strides = _pools(pages, None)
-    if Hkv != 1 or D <= 64:
-        raise ValueError("pages must be [num_pages, page_size, rank + 64]")
-    B, H, T, width = _check_queries(q, pages, D, page_table, lens)
-    there = _elsewhere(stream, q.device)
-    if there is not None:
-        with there:
+    if stream is not None:
+        with _on(stream, q):
             return attn_decode_latent(q, pages, page_table, lens, scale, out, lse, workspace)
-    rank = D - 64
-    workspace, size = _scratch(workspace, decode_latent_workspace_bytes, (B, H, T, width, page, rank), q.device)
-    out, lse = _outputs(q, rank, out, lse)
-    if strides is not None:
-        strides = (ctypes.c_int64 * 2)(strides[0], strides[2])
-    rc = lib().attn_decode_latent(q.data_ptr(), pages.data_ptr(), strides, page_table.data_ptr(), lens.data_ptr(),
-                                  out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size, B, H, T, P, page,
-                                  width, rank, scale, _raw_stream(q.device))
-    if rc != ATTN_OK:
-        raise AttnError(rc, "attn_decode_latent")
-    return out, lse
+    return _checked(_bind().decode_latent(q, pages, page_table, lens, scale, out, lse, workspace),
+                    "attn_decode_latent")
 
 
 def pages_append(k: torch.Tensor, v: Optional[torch.Tensor], k_pages: torch.Tensor,
@@ -584,33 +489,10 @@ def pages_append(k: torch.Tensor, v: Optional[torch.Tensor], k_pages: torch.Tens
     page_size, d] (latent rows: k [B, 1, T, d]) or with heads as above, has
     v = v_pages = None. page_table int32 [B, max_pages], pos and count int32
     [B]."""
-    if (v is None) != (v_pages is None):
-        raise ValueError("v and v_pages go together")
-    Hkv, P, page, d, strides = _pools(k_pages, v_pages)
-    device, shape = k_pages.device, k.shape
-    for t in (k, v):
-        if t is not None and (t.dtype is not torch.bfloat16 or t.device != device or t.shape != shape or
-                              len(shape) != 4 or shape[1] != Hkv or shape[3] != d or t.stride(3) != 1):
-            raise ValueError("k and v must be bf16 tensors [B, Hkv, T, d] on the pages' device, last stride 1")
-    B, _, T, _ = shape
-    width = page_table.shape[-1]
-    _check_int("page_table", page_table, device, B, width)
-    _check_int("pos", pos, device, B)
-    if count is not None:
-        _check_int("count", count, device, B)
-    there = _elsewhere(stream, device)
-    if there is not None:
-        with there:
+    if stream is not None:
+        with _on(stream, k):
             return pages_append(k, v, k_pages, v_pages, page_table, pos, count)
-    if v is None:
-        v_ptr, v_strides, vp_ptr = None, None, None
-    else:
-        v_ptr, v_strides, vp_ptr = v.data_ptr(), _strides(v, 0), v_pages.data_ptr()
-    rc = lib().attn_pages_append(k.data_ptr(), v_ptr, _strides(k, 0), v_strides, k_pages.data_ptr(), vp_ptr, strides,
-                                 page_table.data_ptr(), pos.data_ptr(), None if count is None else count.data_ptr(),
-                                 B, Hkv, T, P, page, width, d, _raw_stream(device))
-    if rc != ATTN_OK:
-        raise AttnError(rc, "attn_pages_append")
+    _checked(_bind().pages_append(k, v, k_pages, v_pages, page_table, pos, count), "attn_pages_append")
 
 
 def pages_workspace_bytes(n: int, num_rows: int, num_pages: int) -> int:
@@ -620,17 +502,6 @@ def pages_workspace_bytes(n: int, num_rows: int, num_pages: int) -> int:
     return r
 
 
-def _check_state(page_table: torch.Tensor, refs: torch.Tensor, device: torch.device) -> Tuple[int, int, int]:
-    """(num_rows, max_pages, num_pages)."""
-    if page_table.dim() != 2 or refs.dim() != 1 or not refs.is_cuda:
-        raise ValueError("page_table must be [num_rows, max_pages] and refs a CUDA tensor [num_pages]")
-    R, width = page_table.shape
-    P = refs.shape[0]
-    _check_int("page_table", page_table, device, R, width)
-    _check_int("refs", refs, device, P)
-    return R, width, P
-
-
 def pages_reserve(page_table: torch.Tensor, refs: torch.Tensor, rows: torch.Tensor, want: torch.Tensor,
                   page_size: int, workspace: Optional[torch.Tensor] = None,
                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
@@ -638,24 +509,10 @@ def pages_reserve(page_table: torch.Tensor, refs: torch.Tensor, rows: torch.Tens
     entries below ceil(want / page_size) without a page get the lowest free
     ones (refs 0), whose counts become 1. Returns granted int32 [n]: 1, or 0
     where the free pages did not suffice or the request was not valid."""
-    device, n = refs.device, rows.numel()
-    R, width, P = _check_state(page_table, refs, device)
-    _check_int("rows", rows, device, n)
-    _check_int("want", want, device, n)
-    there = _elsewhere(stream, device)
-    if there is not None:
-        with there:
+    if stream is not None:
+        with _on(stream, refs):
             return pages_reserve(page_table, refs, rows, want, page_size, workspace)
-    granted = torch.empty_like(rows)
-    if n == 0:
-        return granted
-    workspace, size = _scratch(workspace, pages_workspace_bytes, (n, R, P), device)
-    rc = lib().attn_pages_reserve(page_table.data_ptr(), refs.data_ptr(), rows.data_ptr(), want.data_ptr(),
-                                  granted.data_ptr(), workspace.data_ptr(), size, n, R, P, page_size, width,
-                                  _raw_stream(device))
-    if rc != ATTN_OK:
-        raise AttnError(rc, "attn_pages_reserve")
-    return granted
+    return _checked(_bind().pages_reserve(page_table, refs, rows, want, page_size, workspace), "attn_pages_reserve")
 
 
 def pages_fork(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], page_table: torch.Tensor,
@@ -666,49 +523,21 @@ def pages_fork(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], page_tabl
     pages are shared (refs rise), a partly filled last page is copied to the
     lowest free page. Returns (fresh, granted), int32 [n]: the page taken or
     -1, and 1 or 0. See include/attn.h."""
-    Hkv, P, page, d, strides = _pools(k_pages, v_pages)
-    device, n = k_pages.device, parents.numel()
-    R, width, counts = _check_state(page_table, refs, device)
-    if counts != P:
-        raise ValueError("refs must have one count a page")
-    _check_int("lens", lens, device, R)
-    _check_int("parents", parents, device, n)
-    _check_int("children", children, device, n)
-    there = _elsewhere(stream, device)
-    if there is not None:
-        with there:
+    if stream is not None:
+        with _on(stream, refs):
             return pages_fork(k_pages, v_pages, page_table, lens, refs, parents, children, workspace)
-    fresh, granted = torch.empty_like(parents), torch.empty_like(children)
-    if n == 0:
-        return fresh, granted
-    workspace, size = _scratch(workspace, pages_workspace_bytes, (n, R, P), device)
-    rc = lib().attn_pages_fork(k_pages.data_ptr(), None if v_pages is None else v_pages.data_ptr(), strides,
-                               page_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), parents.data_ptr(),
-                               children.data_ptr(), fresh.data_ptr(), granted.data_ptr(), workspace.data_ptr(), size,
-                               n, R, Hkv, P, page, width, d, _raw_stream(device))
-    if rc != ATTN_OK:
-        raise AttnError(rc, "attn_pages_fork")
-    return fresh, granted
+    return _checked(_bind().pages_fork(k_pages, v_pages, page_table, lens, refs, parents, children, workspace),
+                    "attn_pages_fork")
 
 
 def pages_free(page_table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, rows: torch.Tensor,
                stream: Optional[torch.cuda.Stream] = None) -> None:
     """Empty rows (int32 [n]) in place: their pages' counts fall, their entries
     become -1 and their lengths 0."""
-    device, n = refs.device, rows.numel()
-    R, width, P = _check_state(page_table, refs, device)
-    _check_int("lens", lens, device, R)
-    _check_int("rows", rows, device, n)
-    there = _elsewhere(stream, device)
-    if there is not None:
-        with there:
+    if stream is not None:
+        with _on(stream, refs):
             return pages_free(page_table, lens, refs, rows)
-    if n == 0:
-        return
-    rc = lib().attn_pages_free(page_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), rows.data_ptr(), n, R, P,
-                               width, _raw_stream(device))
-    if rc != ATTN_OK:
-        raise AttnError(rc, "attn_pages_free")
+    _checked(_bind().pages_free(page_table, lens, refs, rows), "attn_pages_free")
 
 
 def pages_compact(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], page_table: torch.Tensor,
@@ -718,27 +547,12 @@ def pages_compact(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], page_t
     """Move the live pages (refs above 0) to the front of the pools, in place,
     and rename them in the table and the counts: in place, or into ``out``
     (table, refs). Returns the number of live pages, int32 [1] on the device."""
-    Hkv, P, page, d, strides = _pools(k_pages, v_pages)
-    device = k_pages.device
-    R, width, counts = _check_state(page_table, refs, device)
-    if counts != P:
-        raise ValueError("refs must have one count a page")
-    table_out, refs_out = (page_table, refs) if out is None else out
-    _check_int("the table in out", table_out, device, R, width)
-    _check_int("the counts in out", refs_out, device, P)
-    there = _elsewhere(stream, device)
-    if there is not None:
-        with there:
+    if stream is not None:
+        with _on(stream, refs):
             return pages_compact(k_pages, v_pages, page_table, refs, out, workspace)
-    live = torch.empty_strided((1,), (1,), dtype=torch.int32, device=device)
-    workspace, size = _scratch(workspace, pages_workspace_bytes, (0, R, P), device)
-    rc = lib().attn_pages_compact(k_pages.data_ptr(), None if v_pages is None else v_pages.data_ptr(), strides,
-                                  page_table.data_ptr(), refs.data_ptr(), table_out.data_ptr(), refs_out.data_ptr(),
-                                  live.data_ptr(), workspace.data_ptr(), size, R, Hkv, P, page, width, d,
-                                  _raw_stream(device))
-    if rc != ATTN_OK:
-        raise AttnError(rc, "attn_pages_compact")
-    return live
+    table_out, refs_out = (page_table, refs) if out is None else out
+    return _checked(_bind().pages_compact(k_pages, v_pages, page_table, refs, table_out, refs_out, workspace),
+                    "attn_pages_compact")
 
 
 def attn_fwd_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float] = None,

@@ -1,4 +1,5 @@
-"""Compile the CUDA library libattn_b200.so in-tree for sm_100a.
+"""Compile the CUDA library libattn_b200.so in-tree for sm_100a, and the Python
+binding attn_bind.so of its entry points for paged caches.
 
 Usage: python -m exact_softmax_attention_04_b200.build_lib [--force] [--verbose]
 """
@@ -13,6 +14,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libattn_b200.so")
+BIND = os.path.join(PKG, "attn_bind.so")
+BIND_SOURCE = os.path.join(CSRC, "bind.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in ("attn_api.cu", "attn_bwd_api.cu", "attn_decode_api.cu",
                                              "attn_paged_api.cu", "attn_pages_api.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("attn_fwd_kernel.cuh", "attn_bwd_kernel.cuh",
@@ -44,16 +47,44 @@ def stale() -> bool:
     return any(os.path.getmtime(f) > t for f in SOURCES + HEADERS)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not stale():
-        return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc()] + NVCC_FLAGS + ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
-    if verbose:
-        cmd += ["-Xptxas", "-v"]
-    cmd += ["-o", tmp] + SOURCES
+def bind_stale() -> bool:
+    if not os.path.exists(BIND):
+        return True
+    t = os.path.getmtime(BIND)
+    return any(os.path.getmtime(f) > t for f in (BIND_SOURCE, os.path.join(ROOT, "include", "attn.h")))
+
+
+def build_bind() -> str:
+    """attn_bind.so, next to the library and against it and torch's."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-o", tmp, BIND_SOURCE, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
+           "-ltorch", "-lc10_cuda", "-lc10", "-L", PKG, "-l:libattn_b200.so", "-Wl,-rpath,$ORIGIN"]
     subprocess.check_call(cmd)
-    os.replace(tmp, LIB)
+    os.replace(tmp, BIND)
+    return BIND
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    if force or stale():
+        tmp = LIB + f".tmp{os.getpid()}"
+        cmd = [_nvcc()] + NVCC_FLAGS + ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
+        if verbose:
+            cmd += ["-Xptxas", "-v"]
+        cmd += ["-o", tmp] + SOURCES
+        subprocess.check_call(cmd)
+        os.replace(tmp, LIB)
+    if force or bind_stale():
+        build_bind()
     return LIB
 
 

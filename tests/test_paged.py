@@ -307,6 +307,52 @@ def test_paged_one_token_shape_and_given_outputs(gpu):
 
 
 @pytest.mark.gpu
+def test_on_a_given_stream(gpu):
+    """What a call allocates belongs to the stream it was given."""
+    k, v, table, ln, g = make(4, 2, 16, 128, [900, 5, 64, 3000], 22, nan=False)
+    q = queries(g, 4, 8, 1, 128)
+    want = run_paged(gpu, q, k, v, table, ln)
+    c = torch.cat([k[:, 0], v[:, 0], k[:, 0], v[:, 0], k[:, 0, :, :64]], -1).contiguous()
+    ql = queries(g, 4, 8, 1, 576)
+    want_l = gpu.attn_decode_latent(ql, c, table, ln, 0.05)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        got = gpu.attn_decode_paged(q, k, v, table, ln, stream=s)
+        got_l = gpu.attn_decode_latent(ql, c, table, ln, 0.05, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    for a, b in zip(got + got_l, want + want_l):
+        assert torch.equal(a, b)
+    assert gpu.sync_status() == gpu.ATTN_OK
+
+
+@pytest.mark.gpu
+def test_binding_refuses_what_does_not_fit(gpu):
+    k, v, table, ln, g = make(2, 2, 16, 64, [50, 900], 23)
+    q = queries(g, 2, 4, 1, 64)
+    ws = torch.empty(16, dtype=torch.uint8, device="cuda")
+    bad = [dict(q=q.float()), dict(q=q.cpu()), dict(q=q[..., :32]), dict(q=q[0, 0]), dict(table=table[0]),
+           dict(table=table.cpu()), dict(lens=ln[:1]), dict(k=k.float()), dict(v=k[..., :32]), dict(k=k[:, 0]),
+           dict(out=torch.empty_like(q, dtype=torch.float32)), dict(lse=torch.empty(2, 4, device="cuda"))]
+    for kw in bad:
+        a = dict(q=q, k=k, v=v, table=table, lens=ln, out=None, lse=None) | kw
+        with pytest.raises(ValueError):
+            gpu.attn_decode_paged(a["q"], a["k"], a["v"], a["table"], a["lens"], out=a["out"], lse=a["lse"])
+    with pytest.raises(TypeError):
+        gpu.attn_decode_paged(q, k, None, table, ln)
+    with pytest.raises(gpu.AttnError):
+        gpu.attn_decode_paged(q, k, v, table, ln, workspace=ws)
+    with pytest.raises(gpu.AttnError):
+        gpu.attn_decode_paged(q, k, v, table, ln, scale=-1.0)
+    with pytest.raises(ValueError):
+        gpu.attn_decode_latent(queries(g, 2, 4, 1, 64), k[:, 0], table, ln, 0.1)
+    # a window of any size is a window
+    o, lse = gpu.attn_decode_paged(q, k, v, table, ln, window=1 << 40)
+    o2, lse2 = gpu.attn_decode_paged(q, k, v, table, ln)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("form", ["paged", "latent"])
 def test_captured_and_replayed_on_another_stream(gpu, form):
     """A captured step reads lengths and tables at replay; two graphs with
