@@ -8,12 +8,22 @@
 //   O^T += C[:, :R]^T P^T   M = R, as blocks of 128, K = 64 positions: the same
 //                           bytes of shared memory as an MN-major operand,
 // so a tile is loaded once and used twice: up to 242 operations a byte at 128
-// heads, where the tensor cores' rate and the memory's are both near. What
-// bounds a block is shared memory: a product reads 2 to 4 KB of C per
-// instruction whatever the number of columns. 64 columns a block is the most
-// that O^T (R x 64 in fp32: half of TMEM at R = 512), q (72 KB) and two tiles of
-// 72 KB leave room for; 128 heads are two blocks that read the same tiles at the
-// same time, the second out of L2.
+// heads, where the tensor cores' rate and the memory's are both near. 64 columns
+// a block is the most that O^T (R x 64 in fp32: half of TMEM at R = 512), q (72 KB)
+// and two tiles of 72 KB leave room for; 128 heads are two blocks that read the
+// same tiles at the same time, the second out of L2.
+//
+// What bounds it. Up to 16 columns HBM: 48 ragged sequences of 1500 to 16384
+// tokens, 16 heads, R = 512: 93 us for 496 MB, 5.3 TB/s (6.0 in the steady state).
+// At 64 columns the two places for tiles: an M = 64 instruction takes 31 cycles
+// at N = 64 (23 at N = 16: its operands' 2 to 4 KB of shared memory a step), an
+// M = 128 one 47, so a tile's 36 + 16 instructions take 2100 cycles, but load (2200
+// to 3400 cycles), scores, softmax (1390) and products take 6100 of a place's time,
+// 3050 a tile: 32 sequences x 128 heads take 85 us against 30 at the rates of the
+// memory and of the tensor cores. Hence the parts of a tile that are freed and
+// loaded one by one, the two softmax groups (103 -> 88 us together with the next),
+// and a warp for each kind of MMAs. Bringing the next tile into L2 by TMA ahead of
+// time made it slower (98 us).
 //
 // Roles as in attn_paged_kernel.cuh. With M = 64, S^T lies in the lower 16 lanes
 // of each quarter of TMEM; read as 8 x 8 blocks, all 32 threads of a warp get a
