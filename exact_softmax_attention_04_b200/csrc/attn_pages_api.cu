@@ -112,7 +112,7 @@ extern "C" int attn_pages_append(const void *k, const void *v, const int64_t *k_
     rc = check_ints({page_table, pos});
     if (rc != ATTN_OK || !aligned(count, 4)) return ATTN_ERR_INVALID;
     if (B > 65535 || static_cast<int64_t>(Hkv) * T > INT_MAX / d) return ATTN_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(Hkv) * a.p.vecs > 65535 * 32 * APPEND_COLS) return ATTN_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(Hkv) * d > (1 << 25)) return ATTN_ERR_UNSUPPORTED;  // (65535 blocks of 1024 in z)
     const int64_t packed[3] = {static_cast<int64_t>(Hkv) * T * d, static_cast<int64_t>(T) * d, d};
     for (int i = 0; i < 2; ++i) {
         const int64_t *s = i == 0 ? k_strides : v_strides;

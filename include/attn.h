@@ -430,7 +430,8 @@ ATTN_API int64_t attn_decode_multi_workspace_bytes(int B, int H, int Hkv, int T,
  *
  * The tables, lengths and counts are read and written by the kernels, so
  * every step can be enqueued, or captured in a CUDA graph, without the host
- * knowing them. All pointers to 32-bit values are 4-byte aligned, pools and
+ * knowing them. The kernels may start behind the tail of the kernel before
+ * them in the stream; they wait for it before they read or write anything. All pointers to 32-bit values are 4-byte aligned, pools and
  * row data 16-byte aligned. The first call on a device allocates its status
  * word (see attn_sync_status): make it before any stream capture.
  */
@@ -459,8 +460,9 @@ ATTN_API int64_t attn_decode_multi_workspace_bytes(int B, int H, int Hkv, int T,
  *                      contents on entry do not matter; calls that may run at
  *                      the same time need one each
  *   page_size        : a power of two, 8 or more; max_pages * page_size at
- *                      most 2^30; H / Hkv * T at most 256; d 64 or 128; others
- *                      give ATTN_ERR_UNSUPPORTED
+ *                      most 2^30, times B at most 2^36; H / Hkv * T at most
+ *                      256; Hkv at most 4096; d 64 or 128; others give
+ *                      ATTN_ERR_UNSUPPORTED
  *
  * Slots at or beyond lens[b], and slots no token's window reaches, may hold
  * any bits, NaN included. Arithmetic as attn_decode; results are identical
@@ -530,8 +532,9 @@ ATTN_API int64_t attn_decode_latent_workspace_bytes(int B, int H, int T, int max
  *   count              : device, int32 [B] clipped to 0 .. T, or NULL: T each
  *   v = v_pages = NULL : a pool of latent rows (Hkv 1, d = rank + 64)
  *   d                  : a multiple of 8 up to 1024, for all entry points
- *                        below; num_pages at most 2^21 - 1; any page_size.
- *                        Others give ATTN_ERR_UNSUPPORTED
+ *                        below; num_pages at most 2^21 - 1; any page_size;
+ *                        B at most 65535, a token's Hkv * d at most 2^25
+ *                        elements. Others give ATTN_ERR_UNSUPPORTED
  * Two tokens of one call must not go to the same slot. Returns as attn_fwd.
  */
 ATTN_API int attn_pages_append(const void *k, const void *v, const int64_t *k_strides,

@@ -45,7 +45,8 @@ def strides(*s):
     (dict(scale=math.inf), 1), (dict(strides=strides(4096, 2048, 127)), 1), (dict(strides=strides(4096, 2048, 132)), 1),
     (dict(strides=strides(4096, 0, 128)), 1),
     (dict(page=4), 2), (dict(page=24), 2), (dict(d=96), 2), (dict(d=256), 2), (dict(width=1 << 27), 2),
-    (dict(H=514, Hkv=2), 2), (dict(B=1 << 20, H=1024, Hkv=512), 2),
+    (dict(H=514, Hkv=2), 2), (dict(B=1 << 20, H=1024, Hkv=512), 2), (dict(B=1 << 12, width=1 << 26), 2),
+    (dict(H=8192, Hkv=8192), 2),
 ])
 def test_decode_paged_refuses_before_any_cuda_call(attn, kw, code):
     a = PAGED | kw
@@ -468,6 +469,47 @@ def test_paged_offsets_past_32_bits(gpu):
     q = queries(g, 2, 16, 1, d)
     o, lse = run_paged(gpu, q, k, v, ids, ln)
     check(o, lse, attention(q, k[used], v[used], torch.arange(8, device="cuda").int().view(2, 4), ln, 1 / math.sqrt(d)))
+
+
+@pytest.mark.gpu
+def test_paged_large_pages_and_a_wide_table(gpu):
+    """Pages of 2^20 tokens, a table of 2^30 positions, 1.3 million tokens."""
+    page, width = 1 << 20, 1 << 10
+    g = torch.Generator(device="cuda")
+    g.manual_seed(31)
+    k, v = (torch.randn((3, 1, page, 64), generator=g, device="cuda").bfloat16() for _ in range(2))
+    table = torch.full((2, width), -1, dtype=torch.int32, device="cuda")
+    table[0, :2] = torch.tensor([2, 0])
+    table[1, 0] = 1
+    ln = torch.tensor([page + 300001, 77], dtype=torch.int32, device="cuda")
+    q = queries(g, 2, 4, 1, 64)
+    for window in (-1, 1000000):
+        o, lse = run_paged(gpu, q, k, v, table, ln, window)
+        check(o, lse, attention(q, k, v, table[:, :2], ln, 1 / 8, window))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", ["paged", "latent"])
+def test_padded_rows_and_the_same_sequence_twice(gpu, form):
+    """Rows without a sequence, whatever their queries hold; rows that share a
+    table row give the same bits where their queries are the same (each tile is
+    a run of its own in a call of this size)."""
+    d = 128 if form == "paged" else 576
+    k, v, table, ln, g = make(3, 1, 16, d, [300, 17, 1000], 32)
+    table = torch.cat([table[[0, 2, 2]], torch.full_like(table[:2], -1), table[1:2]]).contiguous()
+    ln = torch.tensor([300, 1000, 1000, 0, 0, 17], dtype=torch.int32, device="cuda")
+    q = queries(g, 6, 5, 1, d)
+    q[2] = q[1]
+    q[3:5] = float("nan")
+    if form == "paged":
+        o, lse = run_paged(gpu, q, k, v, table, ln)
+        ref = attention(q.nan_to_num(), k, v, table, ln, 1 / math.sqrt(d))
+    else:
+        o, lse = gpu.attn_decode_latent(q, k[:, 0], table, ln, 0.05)
+        assert gpu.sync_status() == gpu.ATTN_OK
+        ref = attention(q.nan_to_num(), k, k[..., :512], table, ln, 0.05)
+    check(o, lse, ref)
+    assert torch.equal(o[1], o[2]) and torch.equal(lse[1], lse[2])
 
 
 # ------------------------------------------------------------------- latent

@@ -47,7 +47,8 @@ STATE = [(dict(table=0), 1), (dict(refs=0), 1), (dict(table=FAKE + 2), 1), (dict
 @pytest.mark.parametrize("kw,code", POOLS + [(dict(k=0), 1), (dict(v=0), 1), (dict(k=FAKE + 2), 1), (dict(B=0), 1),
                                              (dict(T=0), 1), (dict(pos=0), 1), (dict(count=FAKE + 1), 1),
                                              (dict(ks=strides(8, 8, 4)), 1), (dict(ks=strides(8, -8, 8)), 1),
-                                             (dict(B=70000), 2), (dict(T=1 << 30), 2)])
+                                             (dict(B=70000), 2), (dict(T=1 << 30), 2),
+                                             (dict(Hkv=1 << 17, d=1024, page=1, T=1), 2)])
 def test_append_refuses_before_any_cuda_call(attn, kw, code):
     a = A | kw
     assert attn.lib().attn_pages_append(a["k"], a["v"], a["ks"], a["vs"], a["kp"], a["vp"], a["ps"], a["table"],
@@ -356,6 +357,90 @@ def test_many_requests_and_a_large_pool(gpu):
     s.fork(gpu, list(range(0, R, 2)), list(range(1, R, 2)))
     s.free(gpu, list(range(0, R, 3)))
     s.compact(gpu)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(gpu):
+    """A pool of more than 2^32 elements, forked from and compacted between its
+    ends."""
+    P, Hkv, page, d = 34000, 8, 128, 128
+    k = torch.zeros((P, Hkv, page, d), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(33)
+    rows = torch.randn((2, Hkv, page, d), generator=g, device="cuda").bfloat16()
+    k[P - 1], k[P - 2] = rows[0], rows[1]
+    table, lens, refs = int32([[P - 1, P - 2, -1], [-1, -1, -1]]), int32([200, 0]), torch.zeros(P, dtype=torch.int32,
+                                                                                             device="cuda")
+    refs[P - 2:] = 1
+    refs[: P - 4] = 1  # the lowest free page is far up
+    fresh, ok = gpu.pages_fork(k, None, table, lens, refs, int32([0]), int32([1]))
+    assert fresh.tolist() == [P - 4] and ok.tolist() == [1]
+    assert torch.equal(k[P - 4, :, :72], rows[1][:, :72]) and not k[P - 4, :, 72:].any()
+    assert table.tolist() == [[P - 1, P - 2, -1], [P - 1, P - 4, -1]] and refs[P - 1] == 2
+    refs[: P - 4] = 0
+    live = gpu.pages_compact(k, None, table, refs)
+    assert live.tolist() == [3] and table.tolist() == [[2, 1, -1], [2, 0, -1]]
+    assert refs[:4].tolist() == [1, 1, 2, 0] and int(refs.sum()) == 4
+    assert torch.equal(k[2], rows[0]) and torch.equal(k[1], rows[1]) and torch.equal(k[0, :, :72], rows[1][:, :72])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout,Hkv,d", [("hnd", 2, 64), ("latent", 1, 576)])
+def test_captured_and_replayed(gpu, layout, Hkv, d):
+    """A whole round of upkeep in one graph, replayed on states it was not
+    captured on, next to a second graph on its own state and stream."""
+    page, P, R, width, n = 16, 300, 80, 8, 40
+
+    def fresh_state(seed):
+        s = Both(R, width, P, Hkv, page, d, layout, seed)
+        rng = random.Random(seed)
+        s.reserve(gpu, [0, 1, 2], [rng.randrange(1, 100) for _ in range(3)])
+        s.set_lens([rng.randrange(1, 100) if r < 3 else 0 for r in range(R)])
+        return s
+
+    parents, children = [i % 3 for i in range(n)], list(range(3, 3 + n))
+    want = [100 + i % 20 for i in range(n)]
+    ids = [int32(x) for x in (parents, children, want, [4, 5, 0])]
+
+    def round_of(s):
+        fresh, ok = gpu.pages_fork(s.k, s.v, s.table, s.lens, s.refs, ids[0], ids[1])
+        got = gpu.pages_reserve(s.table, s.refs, ids[1], ids[2], page)
+        gpu.pages_free(s.table, s.lens, s.refs, ids[3])
+        live = gpu.pages_compact(s.k, s.v, s.table, s.refs)
+        return fresh, ok, got, live
+
+    states = [fresh_state(seed) for seed in (41, 42)]
+    saved = [[x.clone() for x in (s.table, s.lens, s.refs, *s.pools())] for s in states]
+    round_of(fresh_state(43))
+    torch.cuda.synchronize()
+    graphs = []
+    for s in states:
+        stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            out = round_of(s)
+        graphs.append((graph, stream, out))
+    for s, old in zip(states, saved):
+        for x, y in zip((s.table, s.lens, s.refs, *s.pools()), old):
+            x.copy_(y)
+    torch.cuda.synchronize()
+    for graph, stream, _ in graphs:
+        with torch.cuda.stream(stream):
+            graph.replay()
+    torch.cuda.synchronize()
+    for s, (_, _, (fresh, ok, got, live)) in zip(states, graphs):
+        f, granted, copies = s.book.fork(parents, children)
+        for a, b, m in copies:
+            for x in s.want:
+                as4(x)[b, :, :m] = as4(x)[a, :, :m]
+        assert fresh.tolist() == f and ok.tolist() == granted
+        assert got.tolist() == s.book.reserve(children, want)
+        s.book.free([4, 5, 0])
+        count, moves = s.book.compact()
+        for a, b in moves:
+            for x in s.want:
+                x[b] = x[a]
+        assert live.tolist() == [count]
+        s.same()
 
 
 # ------------------------------------------------------------------ compact
