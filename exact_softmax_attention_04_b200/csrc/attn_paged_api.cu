@@ -131,7 +131,14 @@ int launch_combine(attn_sm100::PagedCombine a, cudaStream_t st)
     a.per_block = 1;
     while (a.per_block < 16 && a.per_block < cols && rows / (2 * a.per_block) >= 2 * kSMs) a.per_block *= 2;
     const int64_t blocks = static_cast<int64_t>(a.split.B) * a.Hkv * a.nblk * ((cols + a.per_block - 1) / a.per_block);
-    return launch_behind(attn_sm100::attn_paged_combine_kernel<TK, DV, NC>, dim3(static_cast<unsigned>(blocks)),
+    // a long row's columns over several blocks while there are few rows: more
+    // groups of lanes then share its segments
+    if constexpr (DV > 128) {
+        if (rows <= 2 * kSMs)
+            return launch_behind(attn_sm100::attn_paged_combine_kernel<TK, DV, 128, NC>,
+                                 dim3(static_cast<unsigned>(blocks), DV / 128), attn_sm100::COMBINE_THREADS, 0, st, a);
+    }
+    return launch_behind(attn_sm100::attn_paged_combine_kernel<TK, DV, DV, NC>, dim3(static_cast<unsigned>(blocks)),
                          attn_sm100::COMBINE_THREADS, 0, st, a);
 }
 

@@ -197,15 +197,16 @@ constexpr int COMBINE_THREADS = 256;
 
 // Joins the segments of `per_block` columns of one (sequence, y) pair:
 //   M = max_s m_s, l = sum_s l_s 2^(m_s - M), O = sum_s O_s 2^(m_s - M) / l.
-// DV / 4 lanes take 16 bytes each of a segment. With few segments the groups of
+// DC of the DV columns of O a block (grid y), DC / 4 lanes with 16 bytes each of
+// a segment. With few segments the groups of
 // lanes take the columns in turn, with many they take the segments, so that a
 // hundred segments of a long sequence are a dozen loads deep. Which segments
 // there are follows from the lengths alone and is worked out while the kernel
 // before is still running.
-template <int TK, int DV, int NC>
+template <int TK, int DV, int DC, int NC>
 __global__ void __launch_bounds__(COMBINE_THREADS) attn_paged_combine_kernel(const PagedCombine a)
 {
-    constexpr int LANES = DV / 4, GROUPS = COMBINE_THREADS / LANES;
+    constexpr int LANES = DC / 4, GROUPS = COMBINE_THREADS / LANES;
     constexpr int FEW = 6;
     __shared__ int red[2][COMBINE_THREADS / 32];
     __shared__ float4 acc_s[GROUPS][LANES];
@@ -257,12 +258,12 @@ __global__ void __launch_bounds__(COMBINE_THREADS) attn_paged_combine_kernel(con
     // run r0 may begin before the sequence; then this is its last segment
     const bool r0_first = deal.start(r0) >= before;
     auto slot = [&](int s, int c) { return paged_slot(r0 + s, y, p.ranges, s > 0 || r0_first) * NC + c; };
-    const int g = tid / LANES, e = tid % LANES;
+    const int g = tid / LANES, e = tid % LANES, col = blockIdx.y * DC + 4 * e;
     const int64_t row0 = (static_cast<int64_t>(b) * a.H + head * G) * p.T + c0;
 
     auto add = [&](float4 &acc, float &l, int64_t at, float ref) {
         const float2 ml = a.part_ml[at];
-        const float4 v = *reinterpret_cast<const float4 *>(a.part_o + at * DV + 4 * e);
+        const float4 v = *reinterpret_cast<const float4 *>(a.part_o + at * DV + col);
         const float f = ex2_approx(ml.x - ref);  // 0 for a segment without a position
         l = fmaf(ml.y, f, l);
         acc.x = fmaf(v.x, f, acc.x);
@@ -277,8 +278,8 @@ __global__ void __launch_bounds__(COMBINE_THREADS) attn_paged_combine_kernel(con
         uint2 w;
         w.x = *reinterpret_cast<const uint32_t *>(&lo);
         w.y = *reinterpret_cast<const uint32_t *>(&hi);
-        *reinterpret_cast<uint2 *>(a.o + (row0 + c) * DV + 4 * e) = w;
-        if (e == 0) a.lse[row0 + c] = l == 0.f ? -CUDART_INF_F : (M + __log2f(l)) * 0.69314718055994531f;
+        *reinterpret_cast<uint2 *>(a.o + (row0 + c) * DV + col) = w;
+        if (col == 0) a.lse[row0 + c] = l == 0.f ? -CUDART_INF_F : (M + __log2f(l)) * 0.69314718055994531f;
     };
 
     grid_dependency_wait();
