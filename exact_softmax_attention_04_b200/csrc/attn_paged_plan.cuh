@@ -261,9 +261,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS) attn_paged_combine_kernel(con
     const int g = tid / LANES, e = tid % LANES, col = blockIdx.y * DC + 4 * e;
     const int64_t row0 = (static_cast<int64_t>(b) * a.H + head * G) * p.T + c0;
 
-    auto add = [&](float4 &acc, float &l, int64_t at, float ref) {
-        const float2 ml = a.part_ml[at];
-        const float4 v = *reinterpret_cast<const float4 *>(a.part_o + at * DV + col);
+    auto add = [](float4 &acc, float &l, const float2 &ml, const float4 &v, float ref) {
         const float f = ex2_approx(ml.x - ref);  // 0 for a segment without a position
         l = fmaf(ml.y, f, l);
         acc.x = fmaf(v.x, f, acc.x);
@@ -286,17 +284,30 @@ __global__ void __launch_bounds__(COMBINE_THREADS) attn_paged_combine_kernel(con
     if (nseg == 1) return;  // one block had the whole sequence
 
     if (nseg <= FEW) {
+        // all of a column's loads before the first sum (34.6 -> 31.8 us for 45
+        // latent sequences x 128 columns; two columns' loads cost more in blocks
+        // that no longer fit an SM)
         for (int c = c_begin + g; c < c_end; c += GROUPS) {
-            float M = -CUDART_INF_F;
+            float2 ml[FEW];
+            float4 v[FEW];
 #pragma unroll
-            for (int s = 0; s < FEW; ++s)
-                if (s < nseg) M = fmaxf(M, a.part_ml[slot(s, c)].x);
+            for (int s = 0; s < FEW; ++s) {
+                ml[s] = make_float2(-CUDART_INF_F, 0.f);
+                v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (s < nseg) {
+                    const int64_t at = slot(s, c);
+                    ml[s] = a.part_ml[at];
+                    v[s] = *reinterpret_cast<const float4 *>(a.part_o + at * DV + col);
+                }
+            }
+            float M = -CUDART_INF_F, l = 0.f;
+#pragma unroll
+            for (int s = 0; s < FEW; ++s) M = fmaxf(M, ml[s].x);
             const float ref = M == -CUDART_INF_F ? 0.f : M;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float l = 0.f;
 #pragma unroll
             for (int s = 0; s < FEW; ++s)
-                if (s < nseg) add(acc, l, slot(s, c), ref);
+                if (s < nseg) add(acc, l, ml[s], v[s], ref);
             write(acc, l, M, c);
         }
         return;
@@ -309,7 +320,10 @@ __global__ void __launch_bounds__(COMBINE_THREADS) attn_paged_combine_kernel(con
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float l = 0.f;
 #pragma unroll 8
-        for (int s = g; s < nseg; s += GROUPS) add(acc, l, slot(s, c), ref);
+        for (int s = g; s < nseg; s += GROUPS) {
+            const int64_t at = slot(s, c);
+            add(acc, l, a.part_ml[at], *reinterpret_cast<const float4 *>(a.part_o + at * DV + col), ref);
+        }
         acc_s[g][e] = acc;
         if (e == 0) l_s[g] = l;
         __syncthreads();
