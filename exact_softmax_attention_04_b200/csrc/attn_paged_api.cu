@@ -133,15 +133,16 @@ int launch_combine(attn_sm100::PagedCombine a, cudaStream_t st)
     const int64_t blocks = static_cast<int64_t>(a.split.B) * a.Hkv * a.nblk * ((cols + a.per_block - 1) / a.per_block);
     // A row's columns over several blocks while there are few rows: more groups of
     // lanes then share its segments (one latent sequence of 60000: 29 -> 23 us;
-    // keys and values of 131072 and 65500 tokens: 41.0 -> 40.3). A block of 32
-    // columns has less to do: with more than two of them an SM, 4 sequences x 28
-    // heads went from 15.8 to 17.4 us.
+    // keys and values of 131072 and 65500 tokens: 41.0 -> 40.3). More
+    // blocks cost more than they share: with three an SM, 4 sequences x 28 heads
+    // of 128 went from 15.8 to 17.4 us, with five, 23 x 16 latent heads of rank
+    // 256 from 15.4 to 17.9.
     constexpr int DC = DV > 128 ? 128 : 32;
     auto launch = [&](auto *kernel, int dc) {
         return launch_behind(kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(DV / dc)),
                              attn_sm100::COMBINE_THREADS, 0, st, a);
     };
-    if (rows * (DV / DC) <= (DV > 128 ? 8 : 2) * kSMs)
+    if (DV > 128 ? rows <= 2 * kSMs : rows * (DV / DC) <= 2 * kSMs)
         return launch(attn_sm100::attn_paged_combine_kernel<TK, DV, DC, NC>, DC);
     return launch(attn_sm100::attn_paged_combine_kernel<TK, DV, DV, NC>, DV);
 }
