@@ -57,7 +57,7 @@ struct LatentCfg {
     static_assert(NC == 16 || NC == 32 || NC == 64, "columns");
     static constexpr int GROUPS = NC == 16 ? 1 : 2;            // softmax warpgroups, which share out the columns
     static constexpr int CG = NC / GROUPS;                     // columns of each
-    static constexpr int THREADS = 96 + 128 * GROUPS;
+    static constexpr int THREADS = 128 + 128 * GROUPS;         // two producers, two MMA warps, the groups
     static constexpr int BOXES = R / 64 + 1;                   // 64-column boxes per row
     static constexpr int BLOCKS = R / 128;                     // blocks of O^T
     // A tile's parts, loaded, used and freed one by one: for each block of O^T
@@ -178,8 +178,11 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
 
     if (count == 0) {
         // fewer tiles than blocks: nothing to do
-    } else if (warp == 0) {
-        // ------------------------------------------------------------ TMA producer
+    } else if (warp == 0 || warp == 3 + 4 * C::GROUPS) {
+        // ------------------------------------------------------------ TMA producers
+        // The parts in turn by two warps: a copy costs its warp some 100 cycles,
+        // and pages of 8 tokens make 24 (R = 256) or 40 of them a tile.
+        const int producer = warp == 0 ? 0 : 1;
         const uint32_t leader = elect_one();
         const int page = 1 << p.pages.page_log2;
         const int npg = max(1, LATENT_TK >> p.pages.page_log2);  // pages per tile, one per lane
@@ -212,6 +215,7 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
             for (int n = 0; n < C::PARTS; ++n) {
                 constexpr int LAST = C::BLOCKS;
                 const int part = n == 0 ? LAST : n - 1, boxes = n == 0 ? 1 : 2;
+                if (n % 2 != producer) continue;
                 if (items >= NST)
                     ok = ok && __all_sync(0xffffffffu, wt.wait(empty(st, part), ((items / NST) - 1) & 1u));
                 if (!ok) break;
@@ -226,7 +230,7 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
             }
             if (!ok) break;
             ++items;
-            if (starts) {
+            if (starts && producer == 0) {
                 if (segs >= 1) ok = __all_sync(0xffffffffu, wt.wait(q_empty, (segs - 1) & 1u));
                 if (!ok) break;
                 if (leader) {
