@@ -14,15 +14,16 @@
 // same tiles at the same time, the second out of L2.
 //
 // What bounds it. Up to 16 columns HBM: 48 ragged sequences of 1500 to 16384
-// tokens, 16 heads, R = 512: 93 us for 496 MB, 5.3 TB/s (6.0 in the steady state).
+// tokens, 16 heads, R = 512: 94 us for 496 MB, 5.3 TB/s (6.0 in the steady state).
 // At 64 columns the two places for tiles: an M = 64 instruction takes 31 cycles
 // at N = 64 (23 at N = 16: its operands' 2 to 4 KB of shared memory a step), an
 // M = 128 one 47, so a tile's 36 + 16 instructions take 2100 cycles, but load (2200
 // to 3400 cycles), scores, softmax (1390) and products take 6100 of a place's time,
-// 3050 a tile: 32 sequences x 128 heads take 85 us against 30 at the rates of the
+// 3050 a tile: 32 sequences x 128 heads take 82 us against 30 at the rates of the
 // memory and of the tensor cores. Hence the parts of a tile that are freed and
 // loaded one by one, the two softmax groups (103 -> 88 us together with the next),
-// and a warp for each kind of MMAs. Bringing the next tile into L2 by TMA ahead of
+// a warp for each kind of MMAs, and two producers (84 -> 82 us; 43 -> 32 us for
+// 8-token pages at R = 256). Bringing the next tile into L2 by TMA ahead of
 // time made it slower (98 us).
 //
 // Roles as in attn_paged_kernel.cuh. With M = 64, S^T lies in the lower 16 lanes
