@@ -321,7 +321,7 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
     } else {
         // ------------------------------------------------------------ softmax
         constexpr int CG = C::CG, NK = CG / 8;      // the group's columns, as blocks of 8
-        const int grp = (warp - 2) / 4, g0 = grp * CG;
+        const int grp = C::GROUPS == 1 ? 0 : (warp - 2) / 4, g0 = grp * CG;
         const int sw = warp % 4;                    // TMEM quarter: positions 16 sw + 0..15 of the tile
         const int rank_lane = sw * 32 + lane;       // row of an O^T block
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(sw * 32) << 16);

@@ -235,7 +235,7 @@ int launch_paged(PagedCall &a)
     p.part_ml = reinterpret_cast<float2 *>(a.workspace + a.l.ml);
     p.part_o = reinterpret_cast<float *>(a.workspace + a.l.o);
     const dim3 grid(static_cast<unsigned>(a.l.ranges), static_cast<unsigned>(a.l.units));
-    if (launch_behind(attn_sm100::attn_paged_kernel<D, NC>, grid, attn_sm100::PAGED_THREADS, C::SMEM_BYTES, a.st, mq, mk,
+    if (launch_behind(attn_sm100::attn_paged_kernel<D, NC>, grid, C::THREADS, C::SMEM_BYTES, a.st, mq, mk,
                       mv, p) != ATTN_OK)
         return ATTN_ERR_CUDA;
     // a sequence of one tile is never split

@@ -14,7 +14,8 @@
 //     of tiles (attn_paged_plan.cuh). A block goes through the segments of its
 //     run without draining the pipeline: the ring of K and V tiles runs on
 //     across them, q is double-buffered.
-//   - more than 16 columns use N = 32, and beyond 32 blocks of 32.
+//   - more than 16 columns use N = 32, with two groups of softmax warps for 16
+//     columns each, and beyond 32 blocks of 32.
 //   - a column's reference maximum, which may be any number that keeps the
 //     exponentials in range, is raised only when the maximum has grown by more
 //     than PAGED_SLACK: O^T in TMEM is then rescaled a few times a segment
@@ -50,7 +51,6 @@ struct PagedParams {
 };
 
 constexpr int PAGED_TK = 128;  // positions per tile
-constexpr int PAGED_THREADS = 192;
 constexpr float PAGED_SLACK = 8.f;
 
 // NC: columns the softmax handles.
@@ -60,6 +60,9 @@ struct PagedCfg {
     static_assert(NC == 4 || NC == 8 || NC == 16 || NC == 32, "columns");
     static constexpr int N = NC <= 16 ? 16 : 32;               // MMA N
     static constexpr int CTAS = NC <= 16 ? 2 : 1;              // blocks per SM
+    static constexpr int GROUPS = NC <= 16 ? 1 : 2;            // softmax warpgroups, which share out the columns
+    static constexpr int CG = NC / GROUPS;                     // columns of each
+    static constexpr int THREADS = 64 + 128 * GROUPS;
     static constexpr int BOXES = D / BOX_COLS;                 // 64-column boxes per row
     static constexpr int BOX_BYTES_T = PAGED_TK * 128;         // [128 positions x 64 columns] bf16
     static constexpr int TILE_BYTES = BOXES * BOX_BYTES_T;     // one K or V tile
@@ -69,7 +72,7 @@ struct PagedCfg {
     static constexpr int P_BYTES = 2 * OPB_BOX;                // N rows x 128 positions
     static constexpr int Q_OFF = NST * TILE_BYTES;             // two q buffers
     static constexpr int P_OFF = Q_OFF + 2 * Q_BYTES;          // P^T
-    static constexpr int RED_OFF = P_OFF + P_BYTES;            // fp32 [3][NC][4 warps]
+    static constexpr int RED_OFF = P_OFF + P_BYTES;            // fp32, by group [3][CG][4 warps]
     static constexpr int COL_OFF = RED_OFF + 3 * 4 * NC * 4;   // float2 [NC]: reciprocal of the sum, maximum
     static constexpr int BAR_OFF = COL_OFF + NC * 8;
     // full[NST], empty[NST], q_full[2], q_empty[2], s_full[2], s_free[2], p_full, pv_done, mma_drain
@@ -110,14 +113,13 @@ __device__ __forceinline__ void paged_tmem_st(uint32_t taddr, const uint32_t (&r
 }
 
 template <int D, int NC>
-__global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
+__global__ void __launch_bounds__((PagedCfg<D, NC>::THREADS), (PagedCfg<D, NC>::CTAS))
     attn_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const PagedParams p)
 {
     using C = PagedCfg<D, NC>;
     using Walk = PagedWalk<PAGED_TK>;
     constexpr int N = C::N;
-    constexpr int NR = NC < 8 ? 8 : NC;  // TMEM columns read per load
     constexpr int NST = C::NST;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -126,8 +128,8 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
     auto ring = [&](int st) { return base + st * C::TILE_BYTES; };
     auto sQ = [&](int qb) { return base + C::Q_OFF + qb * C::Q_BYTES; };
     const uint32_t sP = base + C::P_OFF;
-    float4 *const red = reinterpret_cast<float4 *>(base_ptr + C::RED_OFF);  // [3][NC]: the four warps
-    float2 *const col_s = reinterpret_cast<float2 *>(base_ptr + C::COL_OFF);
+    float4 *const red_all = reinterpret_cast<float4 *>(base_ptr + C::RED_OFF);
+    float2 *const col_all = reinterpret_cast<float2 *>(base_ptr + C::COL_OFF);
     const uint32_t bars = base + C::BAR_OFF;
     auto full = [&](int st) { return bars + 8u * st; };
     auto empty = [&](int st) { return bars + 8u * (NST + st); };
@@ -146,7 +148,6 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
     const int G = p.H / p.Hkv;
     const int head = blockIdx.y / p.nblk;            // key/value head
     const int c0 = (blockIdx.y % p.nblk) * NC;       // first column of this block
-    const int ncol = min(G * T - c0, NC);            // columns in use
     // first q row of sequence b's columns: row c0 of its group
     auto first_row = [&](int b) { return (b * p.H + head * G) * T + c0; };
 
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
         for (int i = lane; i < C::NBAR; i += 32) {
             const uint32_t bar = bars + 8u * i;
             const bool by_softmax = bar == s_free(0) || bar == s_free(1) || bar == p_full;
-            mbar_init(bar, by_softmax ? 4 * 32 : 1);
+            mbar_init(bar, by_softmax ? C::GROUPS * 128 : 1);
         }
         if (lane == 0) *abort_flag = 0;
         fence_mbar_init();
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
     // rows >= NC of P^T meet columns of O^T that nobody reads; NaN there is
     // harmless, but let them be defined
     if constexpr (NC < N) {
-        for (int i = threadIdx.x; i < C::P_BYTES / 16; i += PAGED_THREADS)
+        for (int i = threadIdx.x; i < C::P_BYTES / 16; i += C::THREADS)
             st_shared_v4(sP + i * 16, 0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
     }
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
     grid_dependency_wait();
     grid_dependents_launch();
     // (synchronises the block)
-    const PagedRun run = paged_run<PAGED_TK, PAGED_THREADS>(p.split, blockIdx.x, base_ptr + C::PLAN_OFF);
+    const PagedRun run = paged_run<PAGED_TK, C::THREADS>(p.split, blockIdx.x, base_ptr + C::PLAN_OFF);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const Waiter wt{abort_flag, p.status};
@@ -310,6 +311,12 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
         wt.drain(mma_drain, 0);
     } else {
         // ------------------------------------------------------------ softmax
+        constexpr int CG = C::CG;
+        constexpr int NR = CG < 8 ? 8 : CG;         // TMEM columns read per load
+        const int grp = C::GROUPS == 1 ? 0 : (warp - 2) / 4, g0 = grp * CG;  // the group's first column
+        const int cg0 = c0 + g0, ncol = min(G * T - cg0, CG);
+        float4 *const red = red_all + grp * 3 * CG;  // [3][CG]: the four warps
+        float2 *const col_s = col_all + g0;
         const int sw = warp % 4;                    // TMEM subpartition of this warp
         const int r = sw * 32 + lane;               // position in the tile (= TMEM lane)
         // column of d that O^T holds in this thread's lane (d = 64: lanes
@@ -322,7 +329,7 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
         Walk w = run.walk<PAGED_TK>(p.split);
         auto slot_page = [&]() { return paged_page(p.split, p.pages, w.s, w.b, (w.base() + r) & ~((1 << p.pages.page_log2) - 1)); };
         int id = slot_page();
-        float m_run[NC], l_part[NC];
+        float m_run[CG], l_part[CG];
         bool ok = true;
         int seg_j = run.j;  // where the segment began
         for (int i = 0; i < count; ++i) {
@@ -346,32 +353,32 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
             }
             if (starts) {
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
+                for (int c = 0; c < CG; ++c) {
                     m_run[c] = -CUDART_INF_F;
                     l_part[c] = 0.f;
                 }
                 seg_j = cur.j;
             }
             bool okw = __all_sync(0xffffffffu, wt.wait(s_full(sb), (i / 2) & 1u));
-            float s[NC];
+            float s[CG];
             if (okw) {
                 tc_fence_after();
                 uint32_t sv[NR];
-                paged_tmem_ld<NC>(lane_base + C::S_COL + N * sb, sv);
+                paged_tmem_ld<CG>(lane_base + C::S_COL + N * sb + g0, sv);
                 tc_fence_before();
                 mbar_arrive(s_free(sb));
                 if (plain) {
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) s[c] = __uint_as_float(sv[c]) * sc;
+                    for (int c = 0; c < CG; ++c) s[c] = __uint_as_float(sv[c]) * sc;
                 } else {
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) s[c] = seen ? __uint_as_float(sv[c]) * sc : -CUDART_INF_F;
+                    for (int c = 0; c < CG; ++c) s[c] = seen ? __uint_as_float(sv[c]) * sc : -CUDART_INF_F;
                     if (T > 1) {
                         // (at = len - T + t: seen by the tokens t .. t + window)
                         const int t0 = at - (len - T), t1 = window < 0 ? T : t0 + window;
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) {
-                            const int u = (c0 + c) % T;
+                        for (int c = 0; c < CG; ++c) {
+                            const int u = (cg0 + c) % T;
                             s[c] = u >= t0 && u <= t1 ? s[c] : -CUDART_INF_F;
                         }
                     }
@@ -383,27 +390,27 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
             bool above = false;
             if (okw) {
 #pragma unroll
-                for (int c = 0; c < NC; ++c) above = above || s[c] > m_run[c] + PAGED_SLACK;
+                for (int c = 0; c < CG; ++c) above = above || s[c] > m_run[c] + PAGED_SLACK;
             }
             bool raised = false;
-            float alpha[NC];
+            float alpha[CG];
             // (ok carries a wait that gave up later in the previous tile)
-            if (!__all_sync(0xffffffffu, named_bar_and(1, 4 * 32, okw && ok && !above))) {
+            if (!__all_sync(0xffffffffu, named_bar_and(1 + grp, 4 * 32, okw && ok && !above))) {
                 if (okw) {
                     float mine = -CUDART_INF_F;  // lane c holds column c's maximum
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) {
+                    for (int c = 0; c < CG; ++c) {
                         const float mx = redux_max(s[c]);
                         mine = lane == c ? mx : mine;
                     }
-                    if (lane < NC) reinterpret_cast<float *>(&red[sb * NC + lane])[sw] = mine;
+                    if (lane < CG) reinterpret_cast<float *>(&red[sb * CG + lane])[sw] = mine;
                     __syncwarp();
                 }
-                ok = __all_sync(0xffffffffu, named_bar_and(1, 4 * 32, okw && ok));
+                ok = __all_sync(0xffffffffu, named_bar_and(1 + grp, 4 * 32, okw && ok));
                 if (!ok) break;
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const float4 m4 = red[sb * NC + c];
+                for (int c = 0; c < CG; ++c) {
+                    const float4 m4 = red[sb * CG + c];
                     const float tmax = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
                     const bool up = tmax > m_run[c] + PAGED_SLACK;
                     alpha[c] = up ? ex2_approx(m_run[c] - tmax) : 1.f;
@@ -413,9 +420,9 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
                 }
                 raised = __any_sync(0xffffffffu, raised);
             }
-            float pr[NC];
+            float pr[CG];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
+            for (int c = 0; c < CG; ++c) {
                 // measure from 0 while there is no position, so that no
                 // (-inf) - (-inf) arises; masked positions give 0
                 const float m_ref = (m_run[c] == -CUDART_INF_F) ? 0.f : m_run[c];
@@ -429,10 +436,10 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
             if (okw && !starts && raised) {
                 tc_fence_after();
                 uint32_t o[NR];
-                paged_tmem_ld<NC>(lane_base + C::O_COL, o);
+                paged_tmem_ld<CG>(lane_base + C::O_COL + g0, o);
 #pragma unroll
-                for (int c = 0; c < NC; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[c]);
-                paged_tmem_st<NC>(lane_base + C::O_COL, o);
+                for (int c = 0; c < CG; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[c]);
+                paged_tmem_st<CG>(lane_base + C::O_COL + g0, o);
                 tmem_wait_st();
             }
             // Positions no token sees: their V rows may hold anything (slots
@@ -445,7 +452,7 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
 #pragma unroll
                     for (int bx = 0; bx < C::BOXES; ++bx)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)  // (in an order that spreads the rows over the banks)
+                        for (int e = grp * (8 / C::GROUPS); e < (grp + 1) * (8 / C::GROUPS); ++e)  // (in an order that spreads the rows over the banks)
                             st_shared_v4(ring(st) + bx * C::BOX_BYTES_T + r * 128 + ((e ^ (r & 7)) * 16), 0u, 0u, 0u, 0u);
                 }
                 __syncwarp();
@@ -456,8 +463,8 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
                 const uint32_t col = sP + (r / 64) * C::OPB_BOX +
                                      ((static_cast<uint32_t>((r % 64) / 8)) * 16) + (r % 8) * 2;
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const uint32_t addr = (col + c * 128) ^ (static_cast<uint32_t>(c & 7) << 4);
+                for (int c = 0; c < CG; ++c) {
+                    const uint32_t addr = (col + (g0 + c) * 128) ^ (static_cast<uint32_t>(c & 7) << 4);
                     const unsigned short h = __bfloat16_as_ushort(__float2bfloat16_rn(pr[c]));
                     asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(h) : "memory");
                 }
@@ -470,27 +477,27 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
                 // ---------------------------------------------------- the segment's results
                 float mine = 0.f;
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
+                for (int c = 0; c < CG; ++c) {
                     float sum = l_part[c];
 #pragma unroll
                     for (int o = 16; o >= 1; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     mine = lane == c ? sum : mine;
                 }
-                if (lane < NC) reinterpret_cast<float *>(&red[2 * NC + lane])[sw] = mine;
+                if (lane < CG) reinterpret_cast<float *>(&red[2 * CG + lane])[sw] = mine;
                 if (r == 0) {
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) col_s[c].y = m_run[c];
+                    for (int c = 0; c < CG; ++c) col_s[c].y = m_run[c];
                 }
                 __syncwarp();
                 if (ok) ok = __all_sync(0xffffffffu, wt.wait(pv_done, i & 1u));
-                ok = __all_sync(0xffffffffu, named_bar_and(1, 4 * 32, ok));
+                ok = __all_sync(0xffffffffu, named_bar_and(1 + grp, 4 * 32, ok));
                 if (!ok) break;
                 tc_fence_after();
                 const bool whole = __any_sync(0xffffffffu, seg_j == 0 && cur.last());
-                const int64_t row = first_row(cur.b);
-                const int64_t slot = paged_slot(blockIdx.x, blockIdx.y, p.split.ranges, cur.b == run.b) * NC;
-                if (r < NC) {
-                    const float4 l4 = red[2 * NC + r];
+                const int64_t row = first_row(cur.b) + g0;
+                const int64_t slot = paged_slot(blockIdx.x, blockIdx.y, p.split.ranges, cur.b == run.b) * NC + g0;
+                if (r < CG) {
+                    const float4 l4 = red[2 * CG + r];
                     const float l = (l4.x + l4.y) + (l4.z + l4.w), m = col_s[r].y;
                     if (whole) {
                         col_s[r].x = l == 0.f ? 0.f : 1.f / l;
@@ -500,17 +507,17 @@ __global__ void __launch_bounds__(PAGED_THREADS, (PagedCfg<D, NC>::CTAS))
                     }
                 }
                 __syncwarp();
-                named_bar_sync(1, 4 * 32);
+                named_bar_sync(1 + grp, 4 * 32);
                 // (a short loop: this runs once a segment, and what it costs is
                 // above all fetching its instructions)
 #pragma unroll 1
-                for (int c8 = 0; c8 < NC; c8 += 8) {
+                for (int c8 = 0; c8 < CG; c8 += 8) {
                     uint32_t o[8];
-                    tmem_ld8(lane_base + C::O_COL + c8, o);
+                    tmem_ld8(lane_base + C::O_COL + g0 + c8, o);
                     __nv_bfloat16 *const out = p.o + (row + c8) * D + dcol;
                     float *const part = p.part_o + (slot + c8) * D + dcol;
 #pragma unroll
-                    for (int c = 0; c < (NC < 8 ? NC : 8); ++c) {
+                    for (int c = 0; c < (CG < 8 ? CG : 8); ++c) {
                         const float v = __uint_as_float(o[c]);
                         if (whole) {
                             const float x = v * col_s[c8 + c].x;
