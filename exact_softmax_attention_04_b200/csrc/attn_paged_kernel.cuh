@@ -24,8 +24,8 @@
 // What bounds it: HBM. 64 ragged sequences of 1000 to 8192 tokens (8 key/value
 // heads, 4 query heads each, d = 128, 16-token pages): 181 us for 1.21 GB, 6.66
 // TB/s (a plain copy reads and writes at 6.55). Two sequences of 131072 and 65500
-// tokens, 16 columns: 41 us for 201 MB, of which a third is what every call has,
-// start, pipeline fill and joining (5.1 us for one sequence of 77 tokens). The
+// tokens, 16 columns: 40 us for 201 MB, of which a quarter is what every call has,
+// start, pipeline fill and joining (5.5 us for one sequence of 77 tokens). The
 // ring of 96 KB and two blocks an SM keep 192 KB of loads in flight, four times
 // what the latency asks for. One warp issues both kinds of MMAs: with a warp for
 // each, S(i + 1) no longer waits in front of PV(i), but the ragged batch took 193

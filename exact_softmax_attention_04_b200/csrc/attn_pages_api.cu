@@ -131,15 +131,14 @@ extern "C" int attn_pages_append(const void *k, const void *v, const int64_t *k_
     a.max_pages = max_pages;
     a.vecs = FastDiv(static_cast<uint32_t>(a.p.vecs));
     a.page = FastDiv(static_cast<uint32_t>(page_size));
-    // two tokens a warp where that leaves every SM's warps some
-    const int tok = static_cast<int64_t>(B) * T >= 2 * 64 * kSMs ? 2 : 1;
-    const int tokens = tok * (APPEND_THREADS / 32), units = 32 * APPEND_COLS;
+    // Eight loads a lane in flight: one token of two pools, or two of one (27,000
+    // latent rows: 7.7 us, one token a warp 8.8; keys and values, two tokens a
+    // warp: 34.6 us instead of 33.5 for 25,000, 24.3 instead of 22.0 for 16,000).
+    const int tokens = (v ? 1 : 2) * (APPEND_THREADS / 32), units = 32 * APPEND_COLS;
     const dim3 grid(static_cast<unsigned>((T + tokens - 1) / tokens), static_cast<unsigned>(B),
                     static_cast<unsigned>((Hkv * a.p.vecs + units - 1) / units));
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (tok == 2)
-        return launch_behind(v ? pages_append_kernel<2, 2> : pages_append_kernel<2, 1>, grid, APPEND_THREADS, st, a);
-    return launch_behind(v ? pages_append_kernel<1, 2> : pages_append_kernel<1, 1>, grid, APPEND_THREADS, st, a);
+    return launch_behind(v ? pages_append_kernel<1, 2> : pages_append_kernel<2, 1>, grid, APPEND_THREADS,
+                         static_cast<cudaStream_t>(stream), a);
 }
 
 extern "C" int attn_pages_reserve(int *page_table, int *refs, const int *rows, const int *want, int *granted,

@@ -184,9 +184,9 @@ struct Queries {
 PyObject *pair(Tensor a, Tensor b)
 {
     PyObject *x = THPVariable_Wrap(std::move(a)), *y = THPVariable_Wrap(std::move(b));
-    PyObject *r = PyTuple_Pack(2, x, y);
-    Py_DECREF(x);
-    Py_DECREF(y);
+    PyObject *r = x && y ? PyTuple_Pack(2, x, y) : nullptr;
+    Py_XDECREF(x);
+    Py_XDECREF(y);
     return r;
 }
 
