@@ -14,24 +14,27 @@
 // same tiles at the same time, the second out of L2.
 //
 // What bounds it. Up to 16 columns HBM: 48 ragged sequences of 1500 to 16384
-// tokens, 16 heads, R = 512: 94 us for 496 MB, 5.3 TB/s (6.0 in the steady state).
+// tokens, 16 heads, R = 512: 94 us for 496 MB, 5.3 TB/s.
 // At 64 columns the two places for tiles: an M = 64 instruction takes 31 cycles
 // at N = 64 (23 at N = 16: its operands' 2 to 4 KB of shared memory a step), an
-// M = 128 one 47, so a tile's 36 + 16 instructions take 2100 cycles, but load (2200
-// to 3400 cycles), scores, softmax (1390) and products take 6100 of a place's time,
-// 3050 a tile: 32 sequences x 128 heads take 82 us against 30 at the rates of the
-// memory and of the tensor cores. Hence the parts of a tile that are freed and
-// loaded one by one, the two softmax groups (103 -> 88 us together with the next),
-// a warp for each kind of MMAs, and two producers (84 -> 82 us; 43 -> 32 us for
-// 8-token pages at R = 256). Bringing the next tile into L2 by TMA ahead of
-// time made it slower (98 us).
+// M = 128 one 47, so a tile's 36 + 16 instructions take 2100 cycles, but load,
+// scores, softmax and products in turn take a place for about three times that:
+// 32 sequences x 128 heads of 2000 to 8192 tokens take 90 us against 30 at the
+// rates of the memory and of the tensor cores. Hence the parts of a tile that are
+// freed and loaded one by one, a softmax group for each 16 columns (94 us with two
+// groups of 32, whose chains are longer; R = 256: 62 instead of 70), a warp for each
+// kind of MMAs, and two producers. The maximum is followed exactly, so that a
+// row's largest weight is 1 and exact in bf16 (see attn_paged_kernel.cuh): O^T is
+// rescaled in nearly every tile of a short sequence, and one that may lag by 2^8
+// takes 80 us here. Bringing the next tile into L2 by TMA ahead of time made it
+// slower.
 //
 // Roles as in attn_paged_kernel.cuh. With M = 64, S^T lies in the lower 16 lanes
 // of each quarter of TMEM; read as 8 x 8 blocks, all 32 threads of a warp get a
 // share of them, and P^T goes to shared memory by transposing stores. A thread
 // has 2 positions of a quarter of the columns; maxima over a tile go through three
-// shuffles and then between the four warps. From 32 columns on, two groups of
-// four warps share the columns out and need nothing of one another.
+// shuffles and then between the four warps. The groups of four warps, 16 columns
+// each, need nothing of one another.
 #pragma once
 #include "attn_paged_plan.cuh"
 
@@ -50,14 +53,13 @@ struct LatentParams {
 };
 
 constexpr int LATENT_TK = 64;  // positions per tile
-constexpr float LATENT_SLACK = 8.f;  // as PAGED_SLACK
 
 template <int R, int NC>
 struct LatentCfg {
     static_assert(R == 256 || R == 512, "rank 256 or 512");
     static_assert(NC == 16 || NC == 32 || NC == 64, "columns");
-    static constexpr int GROUPS = NC == 16 ? 1 : 2;            // softmax warpgroups, which share out the columns
-    static constexpr int CG = NC / GROUPS;                     // columns of each
+    static constexpr int CG = 16;                              // columns of a softmax warpgroup
+    static constexpr int GROUPS = NC / CG;
     static constexpr int THREADS = 128 + 128 * GROUPS;         // two producers, two MMA warps, the groups
     static constexpr int BOXES = R / 64 + 1;                   // 64-column boxes per row
     static constexpr int BLOCKS = R / 128;                     // blocks of O^T
@@ -77,7 +79,7 @@ struct LatentCfg {
     static constexpr int Q_OFF = NST * TILE_BYTES;
     static constexpr int P_OFF = Q_OFF + Q_BYTES;
     static constexpr int RED_OFF = P_OFF + P_BYTES;            // fp32 [2][4 warps][NC]
-    static constexpr int COL_OFF = RED_OFF + 2 * 4 * NC * 4;   // float2 [NC]: rescaling factor, maximum
+    static constexpr int COL_OFF = RED_OFF + 2 * 4 * NC * 4;   // float2 [NC]: reciprocal of the sum, maximum
     static constexpr int BAR_OFF = COL_OFF + NC * 8;
     // full[NST][PARTS], empty[NST][PARTS], s_full[2], s_free[2], q_full, q_empty, p_full, pv_done, mma_drain[2]
     static constexpr int NBAR = 2 * NST * PARTS + 10;
@@ -92,26 +94,6 @@ struct LatentCfg {
     static_assert(NST >= 2 && SMEM_BYTES <= 232448, "shared memory");
     static_assert(Q_OFF % 1024 == 0 && P_OFF % 1024 == 0, "operand alignment");
 };
-
-// Reads CG columns of S^T (see tmem_ld_half8).
-template <int CG>
-__device__ __forceinline__ void latent_ld_s(uint32_t taddr, uint32_t (&r)[CG / 2])
-{
-    if constexpr (CG == 16)
-        tmem_ld_half8(taddr, r);
-    else
-        tmem_ld_half16(taddr, r);
-}
-
-template <int W>
-__device__ __forceinline__ void latent_ld_o(uint32_t taddr, uint32_t (&r)[W])
-{
-    if constexpr (W == 16) {
-        tmem_ld16(taddr, r);
-    } else {
-        tmem_ld32(taddr, r);
-    }
-}
 
 template <int R, int NC>
 __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
@@ -369,7 +351,7 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
             if (okw) {
                 tc_fence_after();
                 uint32_t sv[CG / 2];
-                latent_ld_s<CG>(lane_base + NC * sb + g0, sv);
+                tmem_ld_half8(lane_base + NC * sb + g0, sv);
                 tc_fence_before();
                 mbar_arrive(s_free(sb));
 #pragma unroll
@@ -389,14 +371,13 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
                     }
                 }
             }
-            // Does a score exceed its column's reference by more than the slack
-            // (or is there none yet)? Rarely but at a segment's start; then the
-            // group takes the tile's maxima.
+            // Does a score exceed its column's maximum so far? Then the group
+            // takes the tile's maxima.
             bool above = false;
             if (okw) {
 #pragma unroll
                 for (int e = 0; e < CG / 2; ++e)
-                    above = above || s[e] > m_run[e / 4 * 2 + (e & 1)] + LATENT_SLACK;
+                    above = above || s[e] > m_run[e / 4 * 2 + (e & 1)];
             }
             bool raised = false;
             float alpha[CG / 4];
@@ -423,7 +404,7 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
                     float tmax = -CUDART_INF_F;
 #pragma unroll
                     for (int v = 0; v < 4; ++v) tmax = fmaxf(tmax, red[(sb * 4 + v) * CG + 8 * (c / 2) + cc + c % 2]);
-                    const bool up = tmax > m_run[c] + LATENT_SLACK;
+                    const bool up = tmax > m_run[c];
                     alpha[c] = up ? ex2_approx(m_run[c] - tmax) : 1.f;
                     l_part[c] *= alpha[c];
                     m_run[c] = up ? tmax : m_run[c];
@@ -450,25 +431,29 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
             // tiles before i
             if (i >= 1) okw = __all_sync(0xffffffffu, wt.wait(pv_done, (i - 1) & 1u));
             if (raised && !starts) {
-                if (sw == 0 && lane < 4) {
+                // A warp hands its factors round in its row of the maxima of
+                // tile i - 1, which every warp has read by now.
+                float *const factor = red + ((sb ^ 1) * 4 + sw) * CG;
+                if (lane < 4) {
 #pragma unroll
-                    for (int c = 0; c < CG / 4; ++c) col_s[8 * (c / 2) + cc + c % 2].x = alpha[c];
+                    for (int c = 0; c < CG / 4; ++c) factor[8 * (c / 2) + cc + c % 2] = alpha[c];
                 }
                 __syncwarp();
-                okw = __all_sync(0xffffffffu, named_bar_and(1 + grp, 4 * 32, okw));
                 if (okw) {
                     tc_fence_after();
 #pragma unroll 1
-                    for (int blk = 0; blk < C::BLOCKS; ++blk) {
+                    for (int blk = 0; blk < C::BLOCKS; blk += 2) {
                         const uint32_t at = lane_base + C::O_COL + blk * NC + g0;
-                        uint32_t o[CG];
-                        latent_ld_o<CG>(at, o);
+                        uint32_t o[2 * CG], lo[CG], hi[CG];
+                        tmem_ld16_two(at, at + NC, o);
 #pragma unroll
-                        for (int c = 0; c < CG; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * col_s[c].x);
-                        if constexpr (CG == 16)
-                            tmem_st16(at, o);
-                        else
-                            tmem_st32(at, o);
+                        for (int c = 0; c < CG; ++c) {
+                            const float f = factor[c];
+                            lo[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                            hi[c] = __float_as_uint(__uint_as_float(o[CG + c]) * f);
+                        }
+                        tmem_st16(at, lo);
+                        tmem_st16(at + NC, hi);
                     }
                     tmem_wait_st();
                 }

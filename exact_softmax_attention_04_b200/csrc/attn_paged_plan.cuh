@@ -115,7 +115,7 @@ struct PagedRun {
 
 // The block's run, for all its NT threads; `scratch`: PLAN_SCRATCH bytes of
 // shared memory, 16-byte aligned.
-constexpr int PLAN_SCRATCH = 64;
+constexpr int PLAN_SCRATCH = 96;
 
 template <int TK, int NT>
 __device__ __forceinline__ PagedRun paged_run(const PagedSplit &p, int r, void *scratch)
