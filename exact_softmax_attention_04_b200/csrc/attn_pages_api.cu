@@ -16,15 +16,12 @@ namespace {
 using namespace attn_host;
 using namespace attn_sm100;
 
-// The pages' planning kernels sum up to 1024 page counts in 32 bits.
-constexpr int kMaxPages = (1 << 21) - 1;
-
 int check_pools(PagePools *p, const void *k_pages, const void *v_pages, const int64_t *strides, int Hkv,
                 int num_pages, int page_size, int d)
 {
     if (!k_pages || !aligned(k_pages, 16) || !aligned(v_pages, 16)) return ATTN_ERR_INVALID;
     if (Hkv <= 0 || num_pages <= 0 || page_size <= 0 || d <= 0) return ATTN_ERR_INVALID;
-    if (d % 8 != 0 || d > 1024 || num_pages > kMaxPages) return ATTN_ERR_UNSUPPORTED;
+    if (d % 8 != 0 || d > 1024 || num_pages > PLAN_MAX_PAGES) return ATTN_ERR_UNSUPPORTED;
     // a page's 16-byte units are counted in 32 bits
     if (static_cast<int64_t>(2) * Hkv * page_size > INT_MAX / (d / 8)) return ATTN_ERR_UNSUPPORTED;
     const int64_t packed[3] = {static_cast<int64_t>(Hkv) * page_size * d, static_cast<int64_t>(page_size) * d, d};
@@ -95,7 +92,7 @@ int64_t workspace_ints(int n, int num_rows, int num_pages)
 
 extern "C" int64_t attn_pages_workspace_bytes(int n, int num_rows, int num_pages)
 {
-    if (n < 0 || num_rows <= 0 || num_pages <= 0 || num_pages > kMaxPages) return -1;
+    if (n < 0 || num_rows <= 0 || num_pages <= 0 || num_pages > PLAN_MAX_PAGES) return -1;
     return 4 * workspace_ints(n, num_rows, num_pages);
 }
 
@@ -146,7 +143,7 @@ extern "C" int attn_pages_reserve(int *page_table, int *refs, const int *rows, c
                                   int page_size, int max_pages, void *stream)
 {
     if (n < 0 || num_rows <= 0 || num_pages <= 0 || page_size <= 0 || max_pages <= 0) return ATTN_ERR_INVALID;
-    if (num_pages > kMaxPages) return ATTN_ERR_UNSUPPORTED;
+    if (num_pages > PLAN_MAX_PAGES) return ATTN_ERR_UNSUPPORTED;
     if (n == 0) return ATTN_OK;
     if (check_ints({page_table, refs, rows, want, granted, workspace}) != ATTN_OK) return ATTN_ERR_INVALID;
     if (workspace_bytes < static_cast<size_t>(4 * workspace_ints(n, num_rows, num_pages))) return ATTN_ERR_INVALID;

@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) pages_append_kernel(const Appe
 constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_WARPS = PLAN_THREADS / 32;
 constexpr int PLAN_PAGES = 8;          // pages a thread looks at in one go
+constexpr int PLAN_MAX_PAGES = (1 << 21) - 1;  // pages of a pool, so that a block's sums fit in 32 bits
 constexpr int PLAN_SMEM_ROWS = 8192;   // owners of this many rows fit in shared memory
 
 // Inclusive sum over the block of one int per thread; `total` to all threads.
@@ -299,6 +300,27 @@ __device__ __forceinline__ void reserve_fill(const ReserveParams &a, int i)
     });
 }
 
+// The plan's arithmetic. A request counts as its need, or as the whole pool where
+// that is less: it cannot be met then, and what follows begins behind all pages.
+// So the sum of a block's requests fits in 32 bits.
+__host__ __device__ constexpr int reserve_ask(int need, int num_pages)
+{
+    return need < 0 ? 0 : need < num_pages ? need : num_pages;
+}
+static_assert(int64_t(PLAN_THREADS) * reserve_ask(INT32_MAX, PLAN_MAX_PAGES) <= INT32_MAX, "a block's sum");
+
+// Where the pages of a request begin that `before` are asked for in front of.
+__host__ __device__ constexpr int reserve_first(int64_t before, int num_pages)
+{
+    return static_cast<int>(before < num_pages ? before : num_pages);
+}
+
+// With `found` free pages, is the request met?
+__host__ __device__ constexpr bool reserve_met(int need, int first, int found)
+{
+    return need == 0 || (need > 0 && first <= found && need <= found - first);
+}
+
 // The middle part, by one block: which requests are met, and where their pages
 // begin in the list of the lowest free ones.
 __device__ __forceinline__ void reserve_plan(const ReserveParams &a, int *warp_sums, int *owner_s)
@@ -310,18 +332,15 @@ __device__ __forceinline__ void reserve_plan(const ReserveParams &a, int *warp_s
         int need = i < a.n ? a.need[i] : -1;
         if (need >= 0 && owner[a.rows[i]] != i) a.need[i] = need = -1;
         int total;
-        // (a request for more than the pool cannot be met, nor can the ones
-        // behind it: counted as one page more than the pool, the sums stay small)
-        const int ask = min(max(need, 0), a.num_pages + 1);
+        const int ask = reserve_ask(need, a.num_pages);
         const int upto = plan_scan(ask, warp_sums, total);
-        if (i < a.n) a.first[i] = static_cast<int>(min(before + upto - ask, int64_t(a.num_pages) + 1));
+        if (i < a.n) a.first[i] = reserve_first(before + upto - ask, a.num_pages);
         before += total;
     }
     const int wanted = static_cast<int>(min(before, static_cast<int64_t>(a.num_pages)));
     const int found = plan_free_pages(a.t.refs, a.num_pages, wanted, a.list, warp_sums);
     for (int i = threadIdx.x; i < a.n; i += PLAN_THREADS) {
-        const int need = a.need[i], first = a.first[i];
-        a.granted[i] = need >= 0 && (need == 0 || (first <= found && need <= found - first)) ? 1 : 0;
+        a.granted[i] = reserve_met(a.need[i], a.first[i], found) ? 1 : 0;
     }
 }
 
