@@ -81,6 +81,15 @@ int check_ints(std::initializer_list<const void *> ptrs)
     return ATTN_OK;
 }
 
+// The plans step through requests, rows and a row's entries in 32 bits, up to
+// 1024 at a time.
+constexpr int kMaxCount = 1 << 30;
+
+bool countable(int n, int num_rows, int max_pages)
+{
+    return n <= kMaxCount && num_rows <= kMaxCount && max_pages <= kMaxCount;
+}
+
 // Workspace in ints: owners by row, two values and a page per request (or per
 // page for reserve and compact), ranks, a few scalars.
 int64_t workspace_ints(int n, int num_rows, int num_pages)
@@ -93,6 +102,7 @@ int64_t workspace_ints(int n, int num_rows, int num_pages)
 extern "C" int64_t attn_pages_workspace_bytes(int n, int num_rows, int num_pages)
 {
     if (n < 0 || num_rows <= 0 || num_pages <= 0 || num_pages > PLAN_MAX_PAGES) return -1;
+    if (!countable(n, num_rows, 1)) return -1;
     return 4 * workspace_ints(n, num_rows, num_pages);
 }
 
@@ -143,7 +153,7 @@ extern "C" int attn_pages_reserve(int *page_table, int *refs, const int *rows, c
                                   int page_size, int max_pages, void *stream)
 {
     if (n < 0 || num_rows <= 0 || num_pages <= 0 || page_size <= 0 || max_pages <= 0) return ATTN_ERR_INVALID;
-    if (num_pages > PLAN_MAX_PAGES) return ATTN_ERR_UNSUPPORTED;
+    if (num_pages > PLAN_MAX_PAGES || !countable(n, num_rows, max_pages)) return ATTN_ERR_UNSUPPORTED;
     if (n == 0) return ATTN_OK;
     if (check_ints({page_table, refs, rows, want, granted, workspace}) != ATTN_OK) return ATTN_ERR_INVALID;
     if (workspace_bytes < static_cast<size_t>(4 * workspace_ints(n, num_rows, num_pages))) return ATTN_ERR_INVALID;
@@ -177,6 +187,7 @@ extern "C" int attn_pages_fork(void *k_pages, void *v_pages, const int64_t *kv_s
     const int rc = check_pools(&a.p, k_pages, v_pages, kv_strides, Hkv, num_pages, page_size, d);
     if (rc != ATTN_OK) return rc;
     if (n < 0 || num_rows <= 0 || max_pages <= 0) return ATTN_ERR_INVALID;
+    if (!countable(n, num_rows, max_pages)) return ATTN_ERR_UNSUPPORTED;
     if (n == 0) return ATTN_OK;
     if (check_ints({page_table, lens, refs, parents, children, fresh, granted, workspace}) != ATTN_OK)
         return ATTN_ERR_INVALID;
@@ -203,6 +214,7 @@ extern "C" int attn_pages_free(int *page_table, int *lens, int *refs, const int 
                                int num_pages, int max_pages, void *stream)
 {
     if (n < 0 || num_rows <= 0 || num_pages <= 0 || max_pages <= 0) return ATTN_ERR_INVALID;
+    if (!countable(n, num_rows, max_pages)) return ATTN_ERR_UNSUPPORTED;
     if (n == 0) return ATTN_OK;
     if (check_ints({page_table, lens, refs, rows}) != ATTN_OK) return ATTN_ERR_INVALID;
     const PageTables t = {page_table, lens, refs, num_rows, max_pages};

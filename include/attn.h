@@ -562,6 +562,8 @@ ATTN_API int64_t attn_pages_workspace_bytes(int n, int num_rows, int num_pages);
  *   rows, want, granted    : device, int32 [n]
  *   workspace              : device, 4-byte aligned, at least
  *                            attn_pages_workspace_bytes(n, num_rows, num_pages)
+ *   n, num_rows, max_pages : at most 2^30 (fork and free too), else
+ *                            ATTN_ERR_UNSUPPORTED
  */
 ATTN_API int attn_pages_reserve(int *page_table, int *refs, const int *rows, const int *want,
                                 int *granted, void *workspace, size_t workspace_bytes, int n,

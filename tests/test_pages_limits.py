@@ -85,3 +85,29 @@ def test_reserve_counts_up_to_the_largest_pool(plan):
             if g and n > 0:  # its pages lie in the list
                 assert first == at and 0 <= first and first + n <= free
             at += max(n, 0)
+
+
+FAKE = 0x10000  # 16-byte aligned, never dereferenced
+MANY = (1 << 30) + 1
+
+
+@pytest.fixture(scope="module")
+def attn():
+    from exact_softmax_attention_04_b200 import build_lib
+    build_lib.build()
+    import exact_softmax_attention_04_b200 as pkg
+    return pkg
+
+
+@pytest.mark.parametrize("n,rows,width", [(MANY, 8, 8), (4, MANY, 8), (4, 8, MANY), (4, 8, 2 ** 31 - 1)])
+def test_sizes_that_32_bit_loops_cannot_count_are_refused(attn, n, rows, width):
+    """The kernels step through requests, rows and a row's entries in strides of
+    up to 1024, in 32 bits."""
+    lib = attn.lib()
+    p, big = FAKE, 1 << 50
+    assert lib.attn_pages_reserve(p, p, p, p, p, p, big, n, rows, 64, 16, width, None) == 2
+    assert lib.attn_pages_fork(p, p, None, p, p, p, p, p, p, p, p, big, n, rows, 2, 64, 16, width, 128, None) == 2
+    assert lib.attn_pages_free(p, p, p, p, n, rows, 64, width, None) == 2
+    if width == 8:
+        with pytest.raises(ValueError):
+            attn.pages_workspace_bytes(n, rows, 64)
