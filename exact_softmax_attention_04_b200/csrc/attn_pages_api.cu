@@ -102,7 +102,7 @@ int64_t workspace_ints(int n, int num_rows, int num_pages)
 extern "C" int64_t attn_pages_workspace_bytes(int n, int num_rows, int num_pages)
 {
     if (n < 0 || num_rows <= 0 || num_pages <= 0 || num_pages > PLAN_MAX_PAGES) return -1;
-    if (!countable(n, num_rows, 1)) return -1;
+    if (n > 0 && !countable(n, num_rows, 1)) return -1;  // (compact, n = 0, has no such limit)
     return 4 * workspace_ints(n, num_rows, num_pages);
 }
 

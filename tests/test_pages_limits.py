@@ -111,3 +111,7 @@ def test_sizes_that_32_bit_loops_cannot_count_are_refused(attn, n, rows, width):
     if width == 8:
         with pytest.raises(ValueError):
             attn.pages_workspace_bytes(n, rows, 64)
+
+
+def test_compacting_has_no_limit_on_rows(attn):
+    assert attn.pages_workspace_bytes(0, MANY, 64) > 4 * MANY
