@@ -4,7 +4,7 @@
 //   pool(s)      pages of `page_size` token rows per key/value head, d bf16
 //                each; one pool (latent vectors) or two (K and V) of one layout
 //   page_table   [num_rows, max_pages]: row r's position p lies in page
-//                table[r, p / page_size], slot p % page_size; -1: no page
+//                table[r, p / page_size], slot p % page_size; see is_page
 //   lens         [num_rows]: cached tokens of each row
 //   refs         [num_pages]: rows that hold the page; <= 0: the page is free
 //
@@ -67,6 +67,12 @@ struct PageTables {
     int *refs;      // [num_pages]
     int num_rows, max_pages;
 };
+
+// Any other table entry is no page: nothing is read or written through it.
+__device__ __forceinline__ bool is_page(int entry, int num_pages)
+{
+    return static_cast<unsigned>(entry) < static_cast<unsigned>(num_pages);
+}
 
 // Units [at, end) of a part, counted row after row, from src to dst by THREADS
 // threads with UNROLL loads in flight each (one at a time, a copy ran at half
@@ -158,7 +164,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) pages_append_kernel(const Appe
         if (u0 + t >= n || at < 0 || at >= cap) continue;
         const int64_t slot_page = cap <= INT32_MAX ? a.page.div(static_cast<uint32_t>(at)) : at / p.page_size;
         const int page = a.table[static_cast<int64_t>(b) * a.max_pages + slot_page];
-        if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) continue;
+        if (!is_page(page, p.num_pages)) continue;
         const int64_t dst = page * p.page_stride + (at - slot_page * p.page_size) * p.token_stride;
 #pragma unroll
         for (int i = 0; i < APPEND_COLS; ++i) {
@@ -259,11 +265,11 @@ struct ReserveParams {
 // A warp looks at a request's table entries, 32 at a time: `each` is called by
 // all lanes with (entry index, whether the entry is one to fill).
 template <class F>
-__device__ __forceinline__ void reserve_entries(const int *row, int pages, F each)
+__device__ __forceinline__ void reserve_entries(const int *row, int pages, int num_pages, F each)
 {
     for (int j0 = 0; j0 < pages; j0 += 32) {
         const int j = j0 + static_cast<int>(threadIdx.x % 32);
-        each(j, j < pages && row[j] < 0);
+        each(j, j < pages && !is_page(row[j], num_pages));
     }
 }
 
@@ -276,7 +282,7 @@ __device__ __forceinline__ void reserve_count(const ReserveParams &a, int i)
     int need = -1;
     if (static_cast<unsigned>(r) < static_cast<unsigned>(a.t.num_rows) && pages <= a.t.max_pages) {
         need = 0;
-        reserve_entries(a.t.table + static_cast<int64_t>(r) * a.t.max_pages, pages,
+        reserve_entries(a.t.table + static_cast<int64_t>(r) * a.t.max_pages, pages, a.num_pages,
                         [&](int, bool fill) { need += __popc(__ballot_sync(0xffffffffu, fill)); });
     }
     if (threadIdx.x % 32 == 0) a.need[i] = need;
@@ -289,7 +295,7 @@ __device__ __forceinline__ void reserve_fill(const ReserveParams &a, int i)
     if (need <= 0 || !a.granted[i]) return;
     int *const row = a.t.table + static_cast<int64_t>(a.rows[i]) * a.t.max_pages;
     int k = a.first[i];
-    reserve_entries(row, (a.want[i] - 1) / a.page_size + 1, [&](int j, bool fill) {
+    reserve_entries(row, (a.want[i] - 1) / a.page_size + 1, a.num_pages, [&](int j, bool fill) {
         const uint32_t fills = __ballot_sync(0xffffffffu, fill);
         if (fill) {
             const int page = a.list[k + __popc(fills & ((1u << lane) - 1u))];
@@ -418,7 +424,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) pages_fork_plan_kernel(const For
             }
             if (len > 0 && len % a.p.page_size != 0) {
                 const int last = a.t.table[static_cast<int64_t>(from) * a.t.max_pages + len / a.p.page_size];
-                need = static_cast<unsigned>(last) < static_cast<unsigned>(a.p.num_pages) ? 1 : 0;
+                need = is_page(last, a.p.num_pages) ? 1 : 0;
             }
         }
         int total;
@@ -473,7 +479,7 @@ __global__ void __launch_bounds__(COPY_THREADS) pages_fork_kernel(const ForkPara
         for (int j = threadIdx.x; j < full; j += COPY_THREADS) {
             const int shared = from[j];
             to[j] = shared;
-            if (static_cast<unsigned>(shared) < static_cast<unsigned>(p.num_pages)) atomicAdd(&a.t.refs[shared], 1);
+            if (is_page(shared, p.num_pages)) atomicAdd(&a.t.refs[shared], 1);
         }
         for (int j = full + threadIdx.x; j < a.t.max_pages; j += COPY_THREADS) to[j] = j == full ? page : -1;
         if (threadIdx.x == 0) a.t.lens[a.children[i]] = len;
@@ -494,7 +500,7 @@ __global__ void __launch_bounds__(FREE_THREADS) pages_free_kernel(const PageTabl
     int *const row = t.table + static_cast<int64_t>(r) * t.max_pages;
     for (int j = threadIdx.x; j < t.max_pages; j += FREE_THREADS) {
         const int page = atomicExch(&row[j], -1);
-        if (static_cast<unsigned>(page) < static_cast<unsigned>(num_pages)) atomicSub(&t.refs[page], 1);
+        if (is_page(page, num_pages)) atomicSub(&t.refs[page], 1);
     }
     if (threadIdx.x == 0) t.lens[r] = 0;
 }

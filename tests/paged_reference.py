@@ -103,7 +103,7 @@ class Pages:
             if bad:
                 granted.append(0)
                 continue
-            empty = [j for j in range(-(-max(w, 0) // self.page)) if self.table[r][j] < 0]
+            empty = [j for j in range(-(-max(w, 0) // self.page)) if not self.is_page(self.table[r][j])]
             first, asked = asked, asked + len(empty)
             granted.append(int(not empty or asked <= len(free)))
             if granted[-1]:
