@@ -118,7 +118,7 @@ class Pages:
         before_len, before = list(self.lens), [list(r) for r in self.table]
         R, width = len(self.table), len(self.table[0])
         for f, c in zip(parents, children):
-            ok = 0 <= f < R and 0 <= c < R and c not in seen and before_len[c] == 0 and before[c][0] < 0
+            ok = 0 <= f < R and 0 <= c < R and c not in seen and before_len[c] == 0 and not self.is_page(before[c][0])
             if 0 <= c < R:
                 seen.add(c)
             ok = ok and before_len[f] <= width * self.page

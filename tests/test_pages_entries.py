@@ -50,3 +50,18 @@ def test_reserve_leaves_a_row_that_it_refuses(gpu):
     granted = gpu.pages_reserve(table, refs, int32([0, 1]), int32([3, 2]), 1)  # three asked for, two free
     assert granted.tolist() == [0, 0]
     assert table.tolist() == [[9, 4, -1, -1], [0, -1, -1, -1]] and refs.tolist() == [1, 0, 1, 0]
+
+
+@pytest.mark.gpu
+def test_fork_takes_a_child_whose_first_entry_is_no_page(gpu):
+    P, page = 8, 4
+    k = torch.arange(P * page, device="cuda").bfloat16().view(P, page, 1).expand(-1, -1, 8).contiguous()
+    table = int32([[3, 5, -1], [P, -1, -1], [TOP, 7, -1], [6, -1, -1]])
+    lens, refs = int32([6, 0, 0, 0]), int32([0, 0, 0, 1, 0, 1, 0, 0])
+    fresh, granted = gpu.pages_fork(k, None, table, lens, refs, int32([0, 0, 0]), int32([1, 2, 3]))
+    # row 3 holds page 6 in its first entry: not empty
+    assert granted.tolist() == [1, 1, 0] and fresh.tolist() == [0, 1, -1]
+    assert table.tolist() == [[3, 5, -1], [3, 0, -1], [3, 1, -1], [6, -1, -1]]
+    assert lens.tolist() == [6, 6, 6, 0] and refs.tolist() == [1, 1, 0, 3, 0, 1, 0, 0]
+    for p in (0, 1):
+        assert torch.equal(k[p, :2], k[5, :2])
