@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) pages_fork_plan_kernel(const For
             const bool named = static_cast<unsigned>(from) < rows && static_cast<unsigned>(to) < rows &&
                                owner[to] == i;
             // the child holds nothing yet
-            if (named && a.t.lens[to] == 0 &&
+            if (named && a.t.lens[to] <= 0 &&
                 !is_page(a.t.table[static_cast<int64_t>(to) * a.t.max_pages], a.p.num_pages)) {
                 len = max(a.t.lens[from], 0);
                 if (len > static_cast<int64_t>(a.t.max_pages) * a.p.page_size) len = -1;

@@ -65,3 +65,16 @@ def test_fork_takes_a_child_whose_first_entry_is_no_page(gpu):
     assert lens.tolist() == [6, 6, 6, 0] and refs.tolist() == [1, 1, 0, 3, 0, 1, 0, 0]
     for p in (0, 1):
         assert torch.equal(k[p, :2], k[5, :2])
+
+
+@pytest.mark.gpu
+def test_fork_takes_a_child_whose_length_is_negative(gpu):
+    """A negative length counts as 0, a parent's and a child's."""
+    P, page = 8, 4
+    k = torch.zeros((P, page, 8), dtype=torch.bfloat16, device="cuda")
+    table = int32([[3, 5], [-1, -1], [2, -1], [-1, -1]])
+    lens, refs = int32([8, -3, -1, 0]), int32([0, 0, 1, 1, 0, 1, 0, 0])
+    fresh, granted = gpu.pages_fork(k, None, table, lens, refs, int32([0, 2]), int32([1, 3]))
+    assert granted.tolist() == [1, 1] and fresh.tolist() == [-1, -1]
+    assert table.tolist() == [[3, 5], [3, 5], [2, -1], [-1, -1]]
+    assert lens.tolist() == [8, 8, -1, 0] and refs.tolist() == [0, 0, 1, 2, 0, 2, 0, 0]
