@@ -580,8 +580,9 @@ ATTN_API int attn_pages_reserve(int *page_table, int *refs, const int *rows, con
  * full; their rows are copied in every pool, the slots behind them are left
  * as they were. Its other entries become -1. A call takes free pages in the
  * order of its requests. granted[i] becomes 1, or 0 (child left as it was)
- * where no free page is left, a row is out of range, the child is not empty or
- * is named by an earlier request; fresh[i] is the page taken, or -1.
+ * where no free page is left, a row is out of range, the parent's length exceeds
+ * max_pages * page_size, the child is not empty or is named by an earlier
+ * request; fresh[i] is the page taken, or -1.
  *
  *   k_pages, v_pages  : device, the pools (v_pages NULL: one pool)
  *   lens              : device, int32 [num_rows]; others as above
