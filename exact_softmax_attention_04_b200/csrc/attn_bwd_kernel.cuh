@@ -62,7 +62,6 @@ namespace attn_sm100 {
 #ifndef ATTN_BWD_EX2_EMU
 #define ATTN_BWD_EX2_EMU 2
 #endif
-constexpr int STATUS_SMEM_ALIGN = 2;  // device status bit: shared memory base not alignable
 
 struct BwdParams {
     const float *lse2;   // [B*H, n_pad] LSE * log2(e)

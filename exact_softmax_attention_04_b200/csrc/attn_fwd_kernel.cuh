@@ -80,7 +80,9 @@ constexpr int BOX_COLS = 64;                  // bf16 columns per 128-byte swizz
 constexpr int BOX_BYTES = BM * BOX_COLS * 2;  // one [128 x 64] bf16 box: 16 KB
 constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
 constexpr uint64_t DRAIN_LIMIT_NS = 200000000ull;
+// device status bits: a wait gave up; shared memory base not alignable
 constexpr int STATUS_WAIT_TIMEOUT = 1;
+constexpr int STATUS_SMEM_ALIGN = 2;
 
 // The running max is replaced as soon as a tile raises it, so the largest P
 // entry of every row is exactly 1.0 and its bf16 rounding never reaches O. (A

@@ -125,10 +125,16 @@ __global__ void __launch_bounds__((LatentCfg<R, NC>::THREADS), 1)
     const int T = p.split.T;
     const int c0 = blockIdx.y * NC;                  // first column of this block
 
-    if (base % 1024 != 0) {
-        // (the operands' swizzle needs it)
-        if (threadIdx.x == 0) atomicOr(p.status, STATUS_WAIT_TIMEOUT);
+#ifdef ATTN_FAULT_LATENT_SMEM_BASE
+    const bool usable = false;
+#else
+    const bool usable = base % 1024 == 0;  // (the operands' swizzle needs it)
+#endif
+    if (!usable) {
+        // nothing is computed, but the joining kernel finds its plan
+        if (threadIdx.x == 0) atomicOr(p.status, STATUS_SMEM_ALIGN);
         grid_dependency_wait();
+        paged_run<LATENT_TK, C::THREADS>(p.split, blockIdx.x, smem_raw + C::PLAN_OFF);
         return;
     }
     if (warp == 0) {
