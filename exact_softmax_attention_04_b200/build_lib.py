@@ -1,11 +1,13 @@
 """Compile the CUDA library libattn_b200.so in-tree for sm_100a, and the Python
-binding attn_bind.so of its entry points for paged caches.
+binding attn_bind.so of its entry points for paged caches (that only where torch
+is installed).
 
 Usage: python -m exact_softmax_attention_04_b200.build_lib [--force] [--verbose]
 """
 from __future__ import annotations
 
 import argparse
+import importlib.metadata
 import os
 import subprocess
 import sys
@@ -47,6 +49,14 @@ def stale() -> bool:
     return any(os.path.getmtime(f) > t for f in SOURCES + HEADERS)
 
 
+def torch_version():
+    """Of the torch that is installed, or None. (The C library needs none.)"""
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
 def bind_stale() -> bool:
     if not os.path.exists(BIND):
         return True
@@ -84,7 +94,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         subprocess.check_call(cmd)
         os.replace(tmp, LIB)
     if force or bind_stale():
-        build_bind()
+        if torch_version() is None:
+            print(f"torch is not installed: {os.path.basename(BIND)}, the binding for it, is not built", file=sys.stderr)
+        else:
+            build_bind()
     return LIB
 
 
