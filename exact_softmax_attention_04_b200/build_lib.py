@@ -11,6 +11,7 @@ import importlib.metadata
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -57,17 +58,27 @@ def torch_version():
         return None
 
 
+def bind_record() -> str:
+    """The file that says what the binding was built for."""
+    return os.path.join(os.path.dirname(BIND), "_build", "attn_bind.txt")
+
+
+def bind_for() -> str:
+    return f"torch {torch_version()}, {sysconfig.get_config_var('SOABI')}"
+
+
 def bind_stale() -> bool:
-    if not os.path.exists(BIND):
+    if not os.path.exists(BIND) or not os.path.exists(bind_record()):
         return True
+    with open(bind_record()) as f:
+        if f.read() != bind_for():
+            return True
     t = os.path.getmtime(BIND)
     return any(os.path.getmtime(f) > t for f in (BIND_SOURCE, os.path.join(ROOT, "include", "attn.h")))
 
 
 def build_bind() -> str:
     """attn_bind.so, next to the library and against it and torch's."""
-    import sysconfig
-
     import torch
     base = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
@@ -81,6 +92,9 @@ def build_bind() -> str:
            "-ltorch", "-lc10_cuda", "-lc10", "-L", PKG, "-l:libattn_b200.so", "-Wl,-rpath,$ORIGIN"]
     subprocess.check_call(cmd)
     os.replace(tmp, BIND)
+    os.makedirs(os.path.dirname(bind_record()), exist_ok=True)
+    with open(bind_record(), "w") as f:
+        f.write(bind_for())
     return BIND
 
 

@@ -25,3 +25,23 @@ def test_the_library_is_built_without_torch(here, monkeypatch, capsys):
     assert build_lib.build() == build_lib.LIB
     assert not (here / "attn_bind.so").exists()
     assert "torch" in capsys.readouterr().err
+
+
+def test_the_binding_is_stale_after_a_change_of_torch(here, monkeypatch):
+    calls = []
+
+    def compile_(cmd):
+        calls.append(cmd)
+        (here / cmd[cmd.index("-o") + 1]).write_bytes(b"")
+
+    monkeypatch.setattr(build_lib.subprocess, "check_call", compile_)
+    build_lib.build()
+    build_lib.build()
+    assert len(calls) == 1
+    installed = importlib.metadata.version
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: installed(name) + ".other")
+    assert build_lib.bind_stale()
+    build_lib.build()
+    assert len(calls) == 2 and not build_lib.bind_stale()
+    monkeypatch.setattr(build_lib.sysconfig, "get_config_var", lambda name: "other-python")
+    assert build_lib.bind_stale()
