@@ -90,27 +90,23 @@ struct PagedCfg {
     static_assert(CTAS * (SMEM_BYTES + 1024) <= 233472, "blocks per SM");
 };
 
-template <int NC>
-__device__ __forceinline__ void paged_tmem_ld(uint32_t taddr, uint32_t (&r)[NC < 8 ? 8 : NC])
+template <int CG>
+__device__ __forceinline__ void paged_tmem_ld(uint32_t taddr, uint32_t (&r)[CG < 8 ? 8 : CG])
 {
-    if constexpr (NC <= 8) {
+    if constexpr (CG <= 8) {
         tmem_ld8(taddr, r);
-    } else if constexpr (NC == 16) {
-        tmem_ld16(taddr, r);
     } else {
-        tmem_ld32(taddr, r);
+        tmem_ld16(taddr, r);
     }
 }
 
-template <int NC>
-__device__ __forceinline__ void paged_tmem_st(uint32_t taddr, const uint32_t (&r)[NC < 8 ? 8 : NC])
+template <int CG>
+__device__ __forceinline__ void paged_tmem_st(uint32_t taddr, const uint32_t (&r)[CG < 8 ? 8 : CG])
 {
-    if constexpr (NC <= 8) {
+    if constexpr (CG <= 8) {
         tmem_st8(taddr, r);
-    } else if constexpr (NC == 16) {
-        tmem_st16(taddr, r);
     } else {
-        tmem_st32(taddr, r);
+        tmem_st16(taddr, r);
     }
 }
 
