@@ -14,16 +14,17 @@
 // same tiles at the same time, the second out of L2.
 //
 // What bounds it. Up to 16 columns HBM: 48 ragged sequences of 1500 to 16384
-// tokens, 16 heads, R = 512: 94 us for 496 MB, 5.3 TB/s.
+// tokens, 16 heads, R = 512: 95 us for 496 MB, 5.2 TB/s.
 // At 64 columns the two places for tiles: an M = 64 instruction takes 31 cycles
 // at N = 64 (23 at N = 16: its operands' 2 to 4 KB of shared memory a step), an
 // M = 128 one 47, so a tile's 36 + 16 instructions take 2100 cycles, but load,
-// scores, softmax and products in turn take a place for about three times that:
-// 32 sequences x 128 heads of 2000 to 8192 tokens take 90 us against 30 at the
-// rates of the memory and of the tensor cores. Hence the parts of a tile that are
+// scores, softmax, rescaling and products in turn take a place for some 8000, 4000 a
+// tile: 32 sequences x 128 heads of 2000 to 8192 tokens take 90 us against 30 at
+// the rates of the memory and of the tensor cores. Hence the parts of a tile that are
 // freed and loaded one by one, a softmax group for each 16 columns (94 us with two
 // groups of 32, whose chains are longer; R = 256: 62 instead of 70), a warp for each
-// kind of MMAs, and two producers. The maximum is followed exactly, so that a
+// kind of MMAs, and two producers (33 -> 27 us for 23 sequences of 2000 to 8192 tokens
+// in 8-token pages, 32 columns, R = 256). The maximum is followed exactly, so that a
 // row's largest weight is 1 and exact in bf16 (see attn_paged_kernel.cuh): O^T is
 // rescaled in nearly every tile of a short sequence, and one that may lag by 2^8
 // takes 80 us here. Bringing the next tile into L2 by TMA ahead of time made it

@@ -76,10 +76,11 @@ struct Layout {
 };
 
 // Runs per unit: as many as one wave of resident blocks holds, or two or three
-// waves where that evens out a poor fit by an eighth at least (a wave more costs
-// every SM a block's start and end: 11 sequences x 3 heads of 17,000 tokens took
-// 44 us in three waves, which fit 0.7% better, and 34 us in one). There are no more runs than
-// tiles.
+// waves where that evens out a poor fit by an eighth at least. (A wave more costs
+// every SM a block's start and end: 11 sequences x 3 heads of 17,000 tokens at d 64
+// take 37 us in three waves, which fit 0.7% better, and 31 in one. But 80 key/value
+// heads of 32 columns, 2 sequences of 8000 tokens at d 128, take 211 us in one wave,
+// which leaves 68 SMs idle, and 153 in two.) There are no more runs than tiles.
 Layout make_layout(int B, int units, int64_t max_tiles, int resident, int nc, int dv)
 {
     Layout l;
@@ -125,19 +126,22 @@ template <int TK, int DV, int NC>
 int launch_combine(attn_sm100::PagedCombine a, cudaStream_t st)
 {
     // a block of 256 threads for each column while there are few, up to 16
-    // columns a block where that still leaves two blocks an SM (4096 rows of
-    // rank 512: 84.6 us in all; with one block an SM 91.3, with four 86.0)
+    // columns a block where that still leaves two blocks an SM (13 sequences of
+    // 2000 tokens x 3 heads x 32 columns at d 128: 15.5 us in all, with one block
+    // an SM 15.8, with four 17.8; 23 latent sequences of 6000 x 16 heads of rank 256:
+    // 25.7, with one 26.8; 128 sequences of 500 to 4000 x 8 heads at d 64: 33.0, with
+    // one 31.1, with four 34.8)
     const int gt = a.H / a.Hkv * a.split.T, cols = gt < NC ? gt : NC;
     const int64_t rows = static_cast<int64_t>(a.split.B) * a.H * a.split.T;
     a.per_block = 1;
     while (a.per_block < 16 && a.per_block < cols && rows / (2 * a.per_block) >= 2 * kSMs) a.per_block *= 2;
     const int64_t blocks = static_cast<int64_t>(a.split.B) * a.Hkv * a.nblk * ((cols + a.per_block - 1) / a.per_block);
     // A row's columns over several blocks while there are few rows: more groups of
-    // lanes then share its segments (one latent sequence of 60000: 29 -> 23 us;
-    // keys and values of 131072 and 65500 tokens: 41.0 -> 40.3). More
-    // blocks cost more than they share: with three an SM, 4 sequences x 28 heads
-    // of 128 went from 15.8 to 17.4 us, with five, 23 x 16 latent heads of rank
-    // 256 from 15.4 to 17.9.
+    // lanes then share its segments (one latent sequence of 60000 x 16 heads of
+    // rank 512: 31.0 -> 22.8 us; keys and values of 131072 and 65500 tokens, 16
+    // columns at d 128: 41.2 -> 40.2). More blocks cost more than they share: with
+    // up to five an SM, 4 sequences of 2000 tokens x 28 heads of 128 go from 9.2 to
+    // 11.1 us, 23 latent sequences of 6000 x 16 heads of rank 256 from 25.7 to 28.4.
     constexpr int DC = DV > 128 ? 128 : 32;
     auto launch = [&](auto *kernel, int dc) {
         return launch_behind(kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(DV / dc)),

@@ -21,18 +21,22 @@
 //     there: a row's largest weight is then 1 and exact in bf16. A maximum that
 //     may lag by 2^8 rounds it, which for peaked rows is the product's whole
 //     error: 1.2e-3 instead of 0.4e-3 at scores of standard deviation 6. It saves
-//     nothing where the memory bounds the call, but 8 sequences of 8192 tokens
-//     with chunks of 64 tokens x 4 heads for 8 key/value heads take 264 us with
-//     it and 301 without.)
+//     nothing where the memory bounds the call; the chunks of 64 tokens below
+//     take 264 us with it and 301 without.)
 // What bounds it: HBM. 64 ragged sequences of 1000 to 8192 tokens (8 key/value
-// heads, 4 query heads each, d = 128, 16-token pages): 181 us for 1.21 GB, 6.66
+// heads, 4 query heads each, d = 128, 16-token pages): 179 us for 1.21 GB, 6.7
 // TB/s (a plain copy reads and writes at 6.55). Two sequences of 131072 and 65500
 // tokens, 16 columns: 40 us for 201 MB, of which a quarter is what every call has,
-// start, pipeline fill and joining (5.5 us for one sequence of 77 tokens). The
-// ring of 96 KB and two blocks an SM keep 192 KB of loads in flight, four times
-// what the latency asks for. One warp issues both kinds of MMAs: with a warp for
-// each, S(i + 1) no longer waits in front of PV(i), but the ragged batch took 193
-// us.
+// start, pipeline fill and joining (5 us for one sequence of 77 tokens). At d = 64
+// a tile is half the bytes at the same cost of barriers and votes: the ragged batch
+// takes 101 us for 603 MB, 6.0 TB/s, 11 sequences x 3 heads of 17,000 tokens 31 for
+// 144 MB. Beyond 32 columns blocks of 32 take the pages again, out of L2, and a
+// tile's softmax, one after the other with its products, is what counts: the 64
+// newest tokens of 8192 x 4 heads for 8 key/value heads, 8 sequences, take 301 us,
+// 0.23 PFLOP/s. The ring of 96 KB and two blocks an SM keep 192 KB of loads in
+// flight, four times what the latency asks for. One warp issues both kinds of
+// MMAs: with a warp for each, S(i + 1) no longer waits in front of PV(i), but the
+// ragged batch took 193 us instead of 181.
 // A tile's positions that no token sees (before the window, behind the length,
 // or whose table entry is no page, which are not loaded at all) have their
 // scores replaced and their V rows zeroed before the products.

@@ -13,8 +13,8 @@
 // lowest free pages are taken, in the order of the requests).
 //
 // What bounds it: HBM for the copies (8 x 2048 to 4096 tokens of 8 heads x 128
-// appended: 33.5 us for 201 MB read and written, 6.0 TB/s; 3676 of 16384 latent pages
-// compacted: 91 us for 542 MB, 5.9 TB/s, the copy itself 6.7), and for everything
+// appended: 33.2 us for 201 MB read and written, 6.1 TB/s; 3676 of 16384 latent pages
+// compacted: 91 us for 542 MB, 6.0 TB/s, the copy itself 6.7), and for everything
 // small the launches, 2 to 3 us each. Plans are made by one block; its running
 // sums take eight counts a thread or, for compacting, words of 32 pages' bits (the
 // ranks of 16384 pages: 18 -> 8 us).

@@ -431,9 +431,10 @@ ATTN_API int64_t attn_decode_multi_workspace_bytes(int B, int H, int Hkv, int T,
  * The tables, lengths and counts are read and written by the kernels, so
  * every step can be enqueued, or captured in a CUDA graph, without the host
  * knowing them. The kernels may start behind the tail of the kernel before
- * them in the stream; they wait for it before they read or write anything. All pointers to 32-bit values are 4-byte aligned, pools and
- * row data 16-byte aligned. The first call on a device allocates its status
- * word (see attn_sync_status): make it before any stream capture.
+ * them in the stream; they wait for it before they read or write anything. All
+ * pointers to 32-bit values are 4-byte aligned, pools and row data 16-byte
+ * aligned. The first call on a device allocates its status word (see
+ * attn_sync_status): make it before any stream capture.
  */
 
 /*
@@ -465,8 +466,8 @@ ATTN_API int64_t attn_decode_multi_workspace_bytes(int B, int H, int Hkv, int T,
  *                      ATTN_ERR_UNSUPPORTED
  *
  * Slots at or beyond lens[b], and slots no token's window reaches, may hold
- * any bits, NaN included. Arithmetic as attn_decode; results are identical
- * from run to run. Returns as attn_fwd.
+ * any bits, NaN included. Arithmetic as attn_decode (a row's largest weight is
+ * exactly 1); results are identical from run to run. Returns as attn_fwd.
  */
 ATTN_API int attn_decode_paged(const void *q, const void *k_pages, const void *v_pages,
                                const int64_t *kv_strides, const int *page_table, const int *lens,
