@@ -9,6 +9,8 @@
 #include <cstdint>
 #include <mutex>
 
+#include "attn.h"
+
 namespace attn_host {
 
 constexpr int kMaxDevices = 64;
@@ -42,5 +44,25 @@ int effective_block(int n, int block);
 
 // The calling thread's current device, checked against kMaxDevices.
 int current_device(int *dev);
+
+// Launches a kernel that may start while the one before it in the stream still
+// runs, and waits for its results itself.
+template <class... Params, class... Args>
+int launch_behind(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t st, const Args &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return ATTN_OK;
+    cudaGetLastError();  // (reported here)
+    return ATTN_ERR_CUDA;
+}
 
 }  // namespace attn_host

@@ -102,26 +102,6 @@ Layout make_layout(int B, int units, int64_t max_tiles, int resident, int nc, in
     return l;
 }
 
-// A kernel that may start while the one before it in the stream still runs, and
-// waits for its results itself.
-template <class... Params, class... Args>
-int launch_behind(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t st, const Args &...args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return ATTN_OK;
-    cudaGetLastError();  // (reported here)
-    return ATTN_ERR_CUDA;
-}
-
 template <int TK, int DV, int NC>
 int launch_combine(attn_sm100::PagedCombine a, cudaStream_t st)
 {

@@ -53,25 +53,6 @@ PageShape page_shape(const PagePools &p)
     return g;
 }
 
-// A kernel that may start while the one before it in the stream still runs (it
-// waits for its results itself).
-template <class... Params, class... Args>
-int launch_behind(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t st, const Args &...args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return ATTN_OK;
-    cudaGetLastError();  // (reported here)
-    return ATTN_ERR_CUDA;
-}
-
 constexpr int kSMs = 148;
 
 int check_ints(std::initializer_list<const void *> ptrs)
@@ -145,7 +126,7 @@ extern "C" int attn_pages_append(const void *k, const void *v, const int64_t *k_
     const int tokens = (v ? 1 : 2) * (APPEND_THREADS / 32), units = 32 * APPEND_COLS;
     const dim3 grid(static_cast<unsigned>((T + tokens - 1) / tokens), static_cast<unsigned>(B),
                     static_cast<unsigned>((Hkv * a.p.vecs + units - 1) / units));
-    return launch_behind(v ? pages_append_kernel<1, 2> : pages_append_kernel<2, 1>, grid, APPEND_THREADS,
+    return launch_behind(v ? pages_append_kernel<1, 2> : pages_append_kernel<2, 1>, grid, APPEND_THREADS, 0,
                          static_cast<cudaStream_t>(stream), a);
 }
 
@@ -171,11 +152,11 @@ extern "C" int attn_pages_reserve(int *page_table, int *refs, const int *rows, c
     a.num_pages = num_pages;
     a.page_size = page_size;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (n <= RESERVE_FEW) return launch_behind(pages_reserve_kernel, dim3(1), PLAN_THREADS, st, a);
+    if (n <= RESERVE_FEW) return launch_behind(pages_reserve_kernel, dim3(1), PLAN_THREADS, 0, st, a);
     const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(n) * 32 + RESERVE_THREADS - 1) / RESERVE_THREADS);
-    int rc = launch_behind(pages_reserve_count_kernel, dim3(blocks), RESERVE_THREADS, st, a);
-    if (rc == ATTN_OK) rc = launch_behind(pages_reserve_kernel, dim3(1), PLAN_THREADS, st, a);
-    if (rc == ATTN_OK) rc = launch_behind(pages_reserve_fill_kernel, dim3(blocks), RESERVE_THREADS, st, a);
+    int rc = launch_behind(pages_reserve_count_kernel, dim3(blocks), RESERVE_THREADS, 0, st, a);
+    if (rc == ATTN_OK) rc = launch_behind(pages_reserve_kernel, dim3(1), PLAN_THREADS, 0, st, a);
+    if (rc == ATTN_OK) rc = launch_behind(pages_reserve_fill_kernel, dim3(blocks), RESERVE_THREADS, 0, st, a);
     return rc;
 }
 
@@ -204,11 +185,11 @@ extern "C" int attn_pages_fork(void *k_pages, void *v_pages, const int64_t *kv_s
     a.list = a.length + n;
     a.n = n;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (launch_behind(pages_fork_plan_kernel, dim3(1), PLAN_THREADS, st, a) != ATTN_OK) return ATTN_ERR_CUDA;
+    if (launch_behind(pages_fork_plan_kernel, dim3(1), PLAN_THREADS, 0, st, a) != ATTN_OK) return ATTN_ERR_CUDA;
     // eight blocks an SM in all, each with a share of a fork's copy
     const int split = std::max(1, std::min(8 * kSMs / n, 64));
     return launch_behind(pages_fork_kernel, dim3(static_cast<unsigned>(n), static_cast<unsigned>(split)), COPY_THREADS,
-                         st, a);
+                         0, st, a);
 }
 
 extern "C" int attn_pages_free(int *page_table, int *lens, int *refs, const int *rows, int n, int num_rows,
@@ -219,7 +200,7 @@ extern "C" int attn_pages_free(int *page_table, int *lens, int *refs, const int 
     if (n == 0) return ATTN_OK;
     if (check_ints({page_table, lens, refs, rows}) != ATTN_OK) return ATTN_ERR_INVALID;
     const PageTables t = {page_table, lens, refs, num_rows, max_pages};
-    return launch_behind(pages_free_kernel, dim3(static_cast<unsigned>(n)), FREE_THREADS,
+    return launch_behind(pages_free_kernel, dim3(static_cast<unsigned>(n)), FREE_THREADS, 0,
                          static_cast<cudaStream_t>(stream), t, rows, num_pages);
 }
 
@@ -251,6 +232,6 @@ extern "C" int attn_pages_compact(void *k_pages, void *v_pages, const int64_t *k
     a.moves = a.rank + num_pages;
     a.cells = static_cast<int64_t>(num_rows) * max_pages;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (launch_behind(pages_compact_plan_kernel, dim3(1), PLAN_THREADS, st, a) != ATTN_OK) return ATTN_ERR_CUDA;
-    return launch_behind(pages_compact_kernel, dim3(8 * kSMs), COPY_THREADS, st, a);
+    if (launch_behind(pages_compact_plan_kernel, dim3(1), PLAN_THREADS, 0, st, a) != ATTN_OK) return ATTN_ERR_CUDA;
+    return launch_behind(pages_compact_kernel, dim3(8 * kSMs), COPY_THREADS, 0, st, a);
 }
