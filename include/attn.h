@@ -531,6 +531,7 @@ ATTN_API int64_t attn_decode_latent_workspace_bytes(int B, int H, int T, int max
  *   k_pages, v_pages   : device, the pools, written
  *   page_table, pos    : device, int32 [B, max_pages] and [B]
  *   count              : device, int32 [B] clipped to 0 .. T, or NULL: T each
+ *                        (B, T >= 1)
  *   v = v_pages = NULL : a pool of latent rows (Hkv 1, d = rank + 64)
  *   d                  : a multiple of 8 up to 1024, for all entry points
  *                        below; num_pages at most 2^21 - 1; any page_size;
